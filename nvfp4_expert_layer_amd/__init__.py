@@ -377,3 +377,11 @@ def quantize_experts(w13, w2, out=None, start=0):
     moe_nvfp4_quantize_weights(w2, out.w2[start:start + n], out.w2_scale[start:start + n],
                                out.w2_global[start:start + n])
     return out
+
+
+# the layer's steps as operators of their own (include/moe_ops.h)
+from .ops import (BF16, F16, F32, U8, MXFP4Rows, MXFP4Weights, alloc_dispatch_workspace,  # noqa: E402
+                  make_dispatch_problem, make_product_problem, moe_combine, moe_combine_backward, moe_dispatch,
+                  moe_dispatch_backward, moe_dispatch_problem, moe_dispatch_workspace_size, moe_mxfp4_dequantize,
+                  moe_mxfp4_product, moe_mxfp4_product_backward, moe_mxfp4_quantize, moe_product_problem,
+                  quantize_mxfp4_weights)

@@ -19,12 +19,18 @@
 #include <string>
 
 #include "kernels.h"
+#include "status.h"
 
 namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+bool arch_ok(const char* arch) { return arch && std::strncmp(arch, "gfx950", 6) == 0; }
+
+}  // namespace
+
+namespace moe {
+
 int fail(int status, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -39,6 +45,38 @@ int ok() {
     g_last_error.clear();
     return MOE_NVFP4_OK;
 }
+
+int hip_status(hipError_t e, const char* where) {
+    if (e != hipSuccess) return fail(MOE_NVFP4_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
+    return MOE_NVFP4_OK;
+}
+
+// Architecture of the current device, cached per device id.
+int current_arch_ok(int* dev_out) {
+    static std::mutex mu;
+    static int cache[64];  // 0 unknown, 1 gfx950, 2 other
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return fail(MOE_NVFP4_ERR_HIP, "hipGetDevice failed");
+    *dev_out = dev;
+    if (dev < 0 || dev >= 64) return fail(MOE_NVFP4_ERR_HIP, "device id %d out of range", dev);
+    std::lock_guard<std::mutex> lk(mu);
+    if (cache[dev] == 0) {
+        hipDeviceProp_t prop;
+        if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
+            return fail(MOE_NVFP4_ERR_HIP, "hipGetDeviceProperties failed");
+        cache[dev] = arch_ok(prop.gcnArchName) ? 1 : 2;
+    }
+    if (cache[dev] != 1) return fail(MOE_NVFP4_ERR_ARCH, "device %d is not gfx950", dev);
+    return MOE_NVFP4_OK;
+}
+}  // namespace moe
+
+namespace {
+
+using moe::current_arch_ok;
+using moe::fail;
+using moe::hip_status;
+using moe::ok;
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -158,27 +196,6 @@ void make_plan(const moe_nvfp4_problem& p, Plan& pl) {
     pl.total = o;
 }
 
-bool arch_ok(const char* arch) { return arch && std::strncmp(arch, "gfx950", 6) == 0; }
-
-// Architecture of the current device, cached per device id.
-int current_arch_ok(int* dev_out) {
-    static std::mutex mu;
-    static int cache[64];  // 0 unknown, 1 gfx950, 2 other
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return fail(MOE_NVFP4_ERR_HIP, "hipGetDevice failed");
-    *dev_out = dev;
-    if (dev < 0 || dev >= 64) return fail(MOE_NVFP4_ERR_HIP, "device id %d out of range", dev);
-    std::lock_guard<std::mutex> lk(mu);
-    if (cache[dev] == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
-            return fail(MOE_NVFP4_ERR_HIP, "hipGetDeviceProperties failed");
-        cache[dev] = arch_ok(prop.gcnArchName) ? 1 : 2;
-    }
-    if (cache[dev] != 1) return fail(MOE_NVFP4_ERR_ARCH, "device %d is not gfx950", dev);
-    return MOE_NVFP4_OK;
-}
-
 // Compute units of the current device `dev` (cached per device).
 int cu_count(int dev, int* out) {
     static std::mutex mu;
@@ -217,11 +234,6 @@ moe::ExpertWeights to_internal(const moe_nvfp4_weights* w) {
 
 template <class T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
-
-int hip_status(hipError_t e, const char* where) {
-    if (e != hipSuccess) return fail(MOE_NVFP4_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
-    return MOE_NVFP4_OK;
-}
 
 // Routing + permutation into the workspace (or the caller's buffers where given).
 int run_route(const moe_nvfp4_problem& p, const Plan& pl, const void* hidden, const void* gate_w,

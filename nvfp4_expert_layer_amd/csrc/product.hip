@@ -1,0 +1,239 @@
+// MXFP4 products over rows sorted by group, few rows a group (gfx950):
+//   forward   out[r][n]   = sum_k a[r][k] w[g(r)][n][k]
+//   backward  drows[r][k] = sum_n dout[r][n] w[g(r)][n][k]
+// Each group's weight is read once from memory per 64 (backward: 32) of its rows,
+// straight into registers in matrix-core operand order; a workgroup's waves split
+// the reduction and join their sums in LDS in wave order, so nothing depends on
+// timing.  With few rows the weight's bytes are the whole cost.
+//
+// Operand layouts (v_mfma_*_16x16x*): lane l holds row (or column) l % 16 and the
+// K slice of lane group l / 16; the accumulator's element v sits at row 4 (l/16) +
+// v, column l % 16.  The weight is the row operand, tokens are columns, so a lane
+// ends with four consecutive outputs of one token.
+//   W4A4: v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 codes (16 bytes) and one E8M0
+//     scale a lane: one 32-element block as it lies in memory, no decoding.
+//   W4A16: 16 bytes of codes are four operands of v_mfma_f32_16x16x32_bf16;
+//     v_cvt_scalef32_pk_bf16_fp4 decodes a pair with its block scale, exactly.
+#include "device_common.h"
+#include "ops.h"
+#include "product_common.h"
+
+namespace moe {
+
+constexpr int kSWaves = 4;
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+// One pass over the weight tile's K for NT tiles of 16 tokens from row r0.
+template <bool MX, int NR, int NT>
+__device__ __forceinline__ void stream_tiles(const ProductArgs& p, int g, int r0, int re, int n0, f32x4_t* red) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
+    const int KB = p.K / 32;
+    const uint8_t* wrow[NR];
+    const uint8_t* srow[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int64_t n = (int64_t)g * p.N + min(n0 + 16 * i + col, p.N - 1);      // rows past N: any valid row
+        wrow[i] = p.w + n * (p.K / 2);
+        srow[i] = p.w_s + n * KB;
+    }
+    f32x4_t acc[NR][NT];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // units of 256 k (a full 128-byte line of a row's codes), wave-interleaved
+    for (int u = wave; u * 8 < KB; u += kSWaves) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int kb = u * 8 + s * 4 + lg;                  // this lane's block
+            const bool kv = kb < KB;
+            u32x4_t wc[NR];
+            uint32_t ws[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                wc[i] = u32x4_t{0u, 0u, 0u, 0u};
+                ws[i] = 0u;
+                if (kv) {
+                    wc[i] = *reinterpret_cast<const u32x4_t*>(wrow[i] + (int64_t)kb * 16);
+                    ws[i] = srow[i][kb];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int r = r0 + 16 * t + col;
+                const bool v = kv && r < re;
+                if constexpr (MX) {
+                    u32x4_t ac = {0u, 0u, 0u, 0u};
+                    uint32_t as = 0u;
+                    if (v) {
+                        ac = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p.a) +
+                                                               (int64_t)r * (p.K / 2) + (int64_t)kb * 16);
+                        as = p.a_s[(int64_t)r * KB + kb];
+                    }
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) acc[i][t] = mfma_mx16(wc[i], ws[i], ac, as, acc[i][t]);
+                } else {
+                    u32x4_t av[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        av[m] = u32x4_t{0u, 0u, 0u, 0u};
+                        if (v)
+                            av[m] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.a) +
+                                                                      (int64_t)r * p.as + (int64_t)kb * 32 + 8 * m);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        const float sc = __uint_as_float(ws[i] << 23);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            acc[i][t] = mfma_bf16_16(mx_decode8(wc[i][m], sc), av[m], acc[i][t]);
+                    }
+                }
+            }
+        }
+    }
+    // join the waves' sums in wave order
+    __syncthreads();                                            // red's previous readers are done
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) red[((wave * NR + i) * NT + t) * 64 + lane] = acc[i][t];
+    __syncthreads();
+    for (int x = threadIdx.x; x < NR * NT * 64; x += 64 * kSWaves) {
+        f32x4_t s = red[x];
+#pragma unroll
+        for (int w = 1; w < kSWaves; ++w) s += red[w * NR * NT * 64 + x];
+        const int l = x & 63, t = (x >> 6) % NT, i = (x >> 6) / NT;
+        const int r = r0 + 16 * t + (l & 15), n = n0 + 16 * i + 4 * (l >> 4);
+        if (r < re) store4(p.out, p.out_dtype, r * p.os + n, s, p.N - n, p.out_vec);
+    }
+}
+
+template <bool MX, int NR>
+__global__ __launch_bounds__(64 * kSWaves) void product_stream_kernel(ProductArgs p, int by_rank) {
+    __shared__ f32x4_t red[kSWaves * NR * 4 * 64];
+    const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
+    if (g < 0) return;
+    int rb, re;
+    group_rows(p, g, rb, re);
+    const int n0 = blockIdx.x * 16 * NR;
+    for (int r0 = rb; r0 < re;) {
+        const int left = re - r0;
+        if (left > 32) { stream_tiles<MX, NR, 4>(p, g, r0, re, n0, red); r0 += 64; }
+        else if (left > 16) { stream_tiles<MX, NR, 2>(p, g, r0, re, n0, red); r0 += 32; }
+        else { stream_tiles<MX, NR, 1>(p, g, r0, re, n0, red); r0 += 16; }
+    }
+}
+
+hipError_t launch_product_stream(const ProductArgs& p, hipStream_t s) {
+    const int groups = min(p.G, p.M);                           // at most so many hold rows
+    const dim3 grid((p.N + 15) / 16, groups);
+    const int by_rank = p.M < p.G ? 1 : 0;
+    if (p.a_s)
+        hipLaunchKernelGGL((product_stream_kernel<true, 1>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+    else
+        hipLaunchKernelGGL((product_stream_kernel<false, 1>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// backward.  The reduction runs over the weight's rows, so an operand needs eight
+// rows' codes of one column.  A lane takes eight neighbouring columns (one dword of
+// codes) of eight rows, decodes pairs along a row with that row's block scale and
+// regroups them by column (v_perm); operand c of the eight then holds columns
+// 8 i + c for operand row i, and a lane ends with eight consecutive outputs.
+// ---------------------------------------------------------------------------
+template <int NT, bool VECTOR>
+__device__ __forceinline__ void grad_tiles(const ProductArgs& p, int g, int r0, int re, int k0, float* red) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
+    const int KB = p.K / 32, kc = k0 + 8 * col;                 // this lane's columns kc .. kc + 7
+    const bool kv = kc < p.K;                                   // K is a multiple of 32: all eight or none
+    const uint8_t* wbase = p.w + (int64_t)g * p.N * (p.K / 2) + kc / 2;
+    const uint8_t* sbase = p.w_s + (int64_t)g * p.N * KB + kc / 32;
+    const uint16_t* dout = static_cast<const uint16_t*>(p.a);
+    f32x4_t acc[8][NT];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[c][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int ns = wave * 32; ns < p.N; ns += 32 * kSWaves) {
+        const int n = ns + 8 * lg;                              // this lane's rows n .. n + 7
+        uint32_t code[8], sb[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            code[j] = sb[j] = 0u;
+            if (kv && n + j < p.N) {
+                code[j] = *reinterpret_cast<const uint32_t*>(wbase + (int64_t)(n + j) * (p.K / 2));
+                sb[j] = sbase[(int64_t)(n + j) * KB];
+            }
+        }
+        u32x4_t dv[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 16 * t + col;
+            dv[t] = r < re ? load8_bf16<VECTOR>(dout + r * p.as + n, p.N - n) : u32x4_t{0u, 0u, 0u, 0u};
+        }
+        u32x4_t op[8];
+        mx_decode_columns(code, sb, op);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[c][t] = mfma_bf16_16(op[c], dv[t], acc[c][t]);
+    }
+    // red [wave][t][v][c][lane]: a lane's eight columns of output row v
+    __syncthreads();                                            // red's previous readers are done
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[(((wave * NT + t) * 4 + v) * 8 + c) * 64 + lane] = acc[c][t][v];
+    __syncthreads();
+    for (int x = threadIdx.x; x < NT * 4 * 64; x += 64 * kSWaves) {
+        const int l = x & 63, v = (x >> 6) & 3, t = x >> 8;
+        float f[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            f[c] = red[((t * 4 + v) * 8 + c) * 64 + l];
+#pragma unroll
+            for (int w = 1; w < kSWaves; ++w) f[c] += red[(((w * NT + t) * 4 + v) * 8 + c) * 64 + l];
+        }
+        const int r = r0 + 16 * t + (l & 15), k = k0 + 8 * (4 * (l >> 4) + v);
+        if (r < re && k < p.K) {
+            store4(p.out, p.out_dtype, r * p.os + k, f32x4_t{f[0], f[1], f[2], f[3]}, 4, p.out_vec);
+            store4(p.out, p.out_dtype, r * p.os + k + 4, f32x4_t{f[4], f[5], f[6], f[7]}, 4, p.out_vec);
+        }
+    }
+}
+
+template <bool VECTOR>
+__global__ __launch_bounds__(64 * kSWaves) void product_grad_stream_kernel(ProductArgs p, int by_rank) {
+    __shared__ float red[kSWaves * 2 * 32 * 64];
+    const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
+    if (g < 0) return;
+    int rb, re;
+    group_rows(p, g, rb, re);
+    const int k0 = blockIdx.x * 128;
+    for (int r0 = rb; r0 < re;) {
+        if (re - r0 > 16) { grad_tiles<2, VECTOR>(p, g, r0, re, k0, red); r0 += 32; }
+        else { grad_tiles<1, VECTOR>(p, g, r0, re, k0, red); r0 += 16; }
+    }
+}
+
+hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
+    const int groups = min(p.G, p.M);
+    const dim3 grid((p.K + 127) / 128, groups);
+    const int by_rank = p.M < p.G ? 1 : 0;
+    if (dout_vector(p))
+        hipLaunchKernelGGL((product_grad_stream_kernel<true>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+    else
+        hipLaunchKernelGGL((product_grad_stream_kernel<false>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+    return hipGetLastError();
+}
+
+hipError_t launch_product(const ProductArgs& p, hipStream_t s) { return launch_product_stream(p, s); }
+hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s) { return launch_product_grad_stream(p, s); }
+
+}  // namespace moe
