@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe_nvfp4.so")
 SOURCES = ["router.hip", "quant.hip", "gemm.hip", "prefill.hip", "decode.hip", "mid.hip", "dispatch.hip", "mxfp4.hip",
-           "product.hip", "engine.cpp", "ops.cpp"]
+           "product.hip", "product_tiles.hip", "engine.cpp", "ops.cpp"]
 ARCH = "gfx950"
 
 

@@ -71,6 +71,7 @@ struct ProductArgs {
     int out_vec;                  // rows of out start at multiples of four elements' size
 };
 hipError_t launch_product(const ProductArgs& p, hipStream_t s);
+hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s);  // many rows a group
 hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s);   // a: dout bf16 [M][N]
 
 }  // namespace moe

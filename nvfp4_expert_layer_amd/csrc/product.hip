@@ -233,7 +233,13 @@ hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_product(const ProductArgs& p, hipStream_t s) { return launch_product_stream(p, s); }
+// Rows a group (an upper bound of their mean) up to which the weight is streamed.
+constexpr int kStreamRowsMx = 32;
+
+hipError_t launch_product(const ProductArgs& p, hipStream_t s) {
+    const int64_t few = (int64_t)p.G * kStreamRowsMx;
+    return !p.a_s || p.M <= few ? launch_product_stream(p, s) : launch_product_tiles(p, s);
+}
 hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s) { return launch_product_grad_stream(p, s); }
 
 }  // namespace moe

@@ -1,0 +1,322 @@
+// MXFP4 products in tiles, for many rows a group (gfx950).  A tile is 256 rows of
+// one group x 256 outputs; eight waves; the operands come through LDS rings filled
+// straight from global memory (global_load_lds), two or three stages ahead; one
+// workgroup a CU.  The weight is the matrix cores' row operand and tokens are their
+// columns, so that a lane ends with groups of four consecutive outputs of one token
+// (packed stores into the output's staging).
+//
+//   mx_tile_kernel     W4A4: 32x32x64 scaled MFMAs on the codes as they lie in
+//                      memory; 128 k a stage, four stages.
+//   a16_tile_kernel    W4A16: bf16 rows, 64 k a stage, three stages; each wave
+//                      decodes its weight operand in registers (one conversion a
+//                      pair, the block scale within it), then 32x32x16 bf16 MFMAs.
+//   grad_tile_kernel   backward: the reduction runs over the weight's rows, 64 a
+//                      stage; a lane takes four neighbouring columns of eight rows,
+//                      decodes them and regroups the pairs by column.
+//
+// Lane layout of the 32x32 MFMAs: lane l holds row (column) l % 32 and the K slice of
+// lane half l / 32; accumulator value v sits at row 8 (v/4) + 4 (l/32) + v % 4, column
+// l % 32.  K runs in any order as long as both operands use the same one.
+//
+// Past a row's end (K, N not multiples of a stage) lanes load from a block of zeros.
+#include <type_traits>
+
+#include "device_common.h"
+#include "kernels.h"
+#include "ops.h"
+#include "product_common.h"
+
+namespace moe {
+
+constexpr int kTM = 256, kTN = 256, kTWaves = 8, kTThreads = 64 * kTWaves;
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+static __device__ __align__(16) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
+__device__ __forceinline__ void to_lds16(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 4, 0, 0);
+}
+
+// Byte offset of 16-byte unit u of row r in a tile of 128-byte rows: eight
+// consecutive rows put a unit in eight different slots, rows r and r + 8 differ too.
+__device__ __forceinline__ int swz8(int r, int u) { return r * 128 + ((u ^ (r & 7) ^ ((r >> 3) & 1)) << 4); }
+// The same for 64-byte rows of four units.
+__device__ __forceinline__ int swz4(int r, int u) { return r * 64 + ((u ^ (((r >> 1) ^ (r >> 3)) & 3)) << 4); }
+
+struct Tile {
+    int g, rb, re, nt;            // group, its rows [rb, re) of this tile, column block
+};
+
+// Tile of this workgroup, or g = -1.  Tiles are numbered group by group, the NT
+// column blocks of 256 rows together; the eight XCDs (workgroup b runs on XCD b % 8)
+// take contiguous ranges, so that the rows of a tile and the weight of a group are
+// shared within an XCD's L2.  s: 1024 + 16 words of LDS.
+__device__ __forceinline__ Tile find_tile(const ProductArgs& p, int NT, int* s) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int n[2], first[2], rows[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int g = 2 * tid + i;
+        int rb = 0, re = 0;
+        if (g < p.G) group_rows(p, g, rb, re);
+        first[i] = rb;
+        rows[i] = re;
+        n[i] = (re - rb + kTM - 1) / kTM;
+    }
+    const int sum = n[0] + n[1];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(inc, o, 64);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 63) s[wave] = inc;
+    __syncthreads();
+    int at = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kTWaves; ++w) {
+        if (w < wave) at += s[w];
+        total += s[w];
+    }
+    const int64_t all = (int64_t)total * NT, per = (all + 7) >> 3;
+    const int64_t b = blockIdx.x, logical = (b & 7) * per + (b >> 3);
+    const bool live = (b >> 3) < per && logical < all;
+    const int tile = live ? (int)(logical / NT) : -1;
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (tile >= at && tile < at + n[i]) {
+                s[8] = 2 * tid + i;
+                s[9] = first[i] + (tile - at) * kTM;
+                s[10] = min(s[9] + kTM, rows[i]);
+            }
+            at += n[i];
+        }
+    }
+    __syncthreads();
+    Tile t{-1, 0, 0, 0};
+    if (live) t = Tile{s[8], s[9], s[10], (int)(logical - (int64_t)tile * NT)};
+    __syncthreads();                                     // s is free again
+    return t;
+}
+
+static int64_t tile_grid(const ProductArgs& p, int NT) {
+    // groups' partial tiles: at most one each
+    const int64_t tiles = p.M / kTM + min(p.G, p.M);
+    return (tiles * NT + 7) / 8 * 8;
+}
+
+// ---------------------------------------------------------------------------
+// Output staging: bf16 / f16 [256 tokens][264] in LDS (the row pitch spreads 32 rows'
+// 8-byte pieces over all banks), then 16-byte row pieces to memory; fp32 goes straight
+// from the accumulators, 16 bytes a lane.
+// ---------------------------------------------------------------------------
+constexpr int kYS = 264;
+
+__device__ __forceinline__ void stage4(const ProductArgs& p, uint8_t* smem, const Tile& t, int row, int col, int width,
+                                       float a, float b, float c, float d) {
+    if (p.out_dtype == kF32) {
+        if (t.rb + row < t.re)
+            store4(p.out, kF32, (t.rb + row) * p.os + t.nt * kTN + col, f32x4_t{a, b, c, d},
+                   width - t.nt * kTN - col, p.out_vec);
+        return;
+    }
+    u32x2_t v;
+    if (p.out_dtype == kBF16) v = u32x2_t{f32x2_to_bf16x2(a, b), f32x2_to_bf16x2(c, d)};
+    else v = u32x2_t{f32_to_f16_bits(a) | (f32_to_f16_bits(b) << 16), f32_to_f16_bits(c) | (f32_to_f16_bits(d) << 16)};
+    *reinterpret_cast<u32x2_t*>(smem + (row * kYS + col) * 2) = v;
+}
+
+__device__ __forceinline__ void store_staged(const ProductArgs& p, const uint8_t* smem, const Tile& t, int width) {
+    if (p.out_dtype == kF32) return;
+    __syncthreads();
+    const int nrow = t.re - t.rb, ncol = min(kTN, width - t.nt * kTN);
+    uint16_t* out = static_cast<uint16_t*>(p.out) + t.rb * p.os + t.nt * kTN;
+    const bool vec = p.os % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+    for (int x = threadIdx.x; x < kTM * (kTN / 8); x += kTThreads) {
+        const int row = x >> 5, c = (x & 31) * 8;
+        if (row >= nrow) break;                          // rows grow with x
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + (row * kYS + c) * 2);
+        if (vec && c + 8 <= ncol) {
+            *reinterpret_cast<u32x4_t*>(out + row * p.os + c) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < ncol) out[row * p.os + c + i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// W4A4
+// ---------------------------------------------------------------------------
+constexpr int kMxStages = 4;
+constexpr int kMxCodes = 256 * 64, kMxScales = 256 * 4;     // an operand's 128 k of a stage
+constexpr int kMxSlot = 2 * kMxCodes + 2 * kMxScales;       // weight codes | row codes | weight scales | row scales
+constexpr int kMxLds = kMxStages * kMxSlot;                 // 136 KB
+
+template <int OPSEL>
+__device__ __forceinline__ f32x16_t mfma_mx32(const u32x4_t& a, uint32_t as, const u32x4_t& b, uint32_t bs,
+                                              const f32x16_t& c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, 4, 4, OPSEL, (int)as,
+                                                           OPSEL, (int)bs);
+}
+
+// ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales).
+template <bool ALIGNED>
+__global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const Tile t = find_tile(p, (p.N + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
+    if (t.g < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5;
+    const int wm = wave >> 2, wn = wave & 3;             // rows 128 wm .. +128, outputs 64 wn .. +64
+    const int KB = p.K / 32, nc = (KB + 3) / 4, n0 = t.nt * kTN;
+    const uint8_t* acodes = static_cast<const uint8_t*>(p.a);
+    // rows and outputs past the tile's end: any valid row (their results are not stored)
+    auto arow = [&](int r) { return (int64_t)min(t.rb + r, t.re - 1); };
+    auto wrow = [&](int r) { return (int64_t)t.g * p.N + min(n0 + r, p.N - 1); };
+
+    // loads of a stage: per operand 16 KB of codes, two of 1 KB a wave: load q of wave w
+    // fills rows 16 (2 w + q) .. +16, lane i row i / 4, slot i % 4, which holds unit
+    // (i % 4) ^ f(row) of the stage (swz4); scales: 256 bytes a wave, waves 0-3 the
+    // weight's rows 64 w .. +64, waves 4-7 the rows'
+    const uint8_t *csrc[2], *asrc[2];
+    int cu[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = (wave * 2 + q) * 16 + (lane >> 2);
+        cu[q] = (lane & 3) ^ (((r >> 1) ^ (r >> 3)) & 3);
+        csrc[q] = p.w + wrow(r) * (p.K / 2) + cu[q] * 16;
+        asrc[q] = acodes + arow(r) * (p.K / 2) + cu[q] * 16;
+    }
+    const int srow = (wave & 3) * 64 + lane;
+    const uint8_t* ssrc = wave < 4 ? p.w_s + wrow(srow) * KB : p.a_s + arow(srow) * KB;
+    const int sdst = 2 * kMxCodes + (wave < 4 ? 0 : kMxScales) + (wave & 3) * 256;
+
+    auto issue = [&](int c, int slot) {
+        uint8_t* base = smem + slot * kMxSlot;
+        const bool whole = ALIGNED || c * 4 + 4 <= KB;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const bool in = whole || c * 4 + cu[q] < KB;
+            to_lds16(in ? csrc[q] + (int64_t)c * 64 : (const uint8_t*)kZeros, base + (wave * 2 + q) * 1024);
+            to_lds16(in ? asrc[q] + (int64_t)c * 64 : (const uint8_t*)kZeros, base + kMxCodes + (wave * 2 + q) * 1024);
+        }
+        if (ALIGNED) to_lds4(ssrc + (int64_t)c * 4, base + sdst);
+    };
+    // unaligned scale rows: bytes through a register
+    auto scale_bytes = [&](int c) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c * 4 + i < KB) v |= (uint32_t)ssrc[c * 4 + i] << (8 * i);
+        return v;
+    };
+    auto put_scales = [&](uint32_t v, int slot) {
+        *reinterpret_cast<uint32_t*>(smem + slot * kMxSlot + sdst + lane * 4) = v;
+    };
+
+    f32x16_t acc[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
+    const int nvi = max(0, min(4, (t.re - t.rb - wm * 128 + 31) >> 5));      // 32-row blocks with rows
+    const bool cols = n0 + wn * 64 < p.N;
+    const int r32 = lane & 31;
+
+    // Stage c sits in slot c % 4 and is three stages ahead when issued, into the slot
+    // that the last barrier freed; past the end valid stages are loaded again, so each
+    // step issues the same five loads and the wait leaves the two newer stages in
+    // flight.  Lane half h of MFMA m takes block 2 h + m of the stage's four.
+    auto kloop = [&](auto nv_c) {
+        constexpr int NV = decltype(nv_c)::value;
+        for (int c = 0; c < nc; ++c) {
+            issue(min(c + 3, nc - 1), (c + 3) & 3);
+            uint32_t pend = 0;
+            if (!ALIGNED && c + 1 < nc) pend = scale_bytes(c + 1);
+            if constexpr (NV > 0) {
+                const uint8_t* S = smem + (c & 3) * kMxSlot;
+                uint32_t ws[2], as[4];
+                u32x4_t wv[2][2], av[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = wn * 64 + j * 32 + r32;
+                    ws[j] = *reinterpret_cast<const uint32_t*>(S + 2 * kMxCodes + r * 4) >> (16 * h);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) wv[m][j] = *reinterpret_cast<const u32x4_t*>(S + swz4(r, 2 * h + m));
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int r = wm * 128 + i * 32 + r32;
+                    as[i] = *reinterpret_cast<const uint32_t*>(S + 2 * kMxCodes + kMxScales + r * 4) >> (16 * h);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        av[m][i] = *reinterpret_cast<const u32x4_t*>(S + kMxCodes + swz4(r, 2 * h + m));
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_mx32<0>(wv[0][j], ws[j], av[0][i], as[i], acc[j][i]);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_mx32<1>(wv[1][j], ws[j], av[1][i], as[i], acc[j][i]);
+            }
+            if (ALIGNED) {
+                asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            } else {
+                put_scales(pend, (c + 1) & 3);
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            }
+        }
+    };
+    issue(0, 0);
+    issue(min(1, nc - 1), 1);
+    issue(min(2, nc - 1), 2);
+    if (!ALIGNED) put_scales(scale_bytes(0), 0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    switch (cols ? nvi : 0) {
+        case 4: kloop(std::integral_constant<int, 4>{}); break;
+        case 3: kloop(std::integral_constant<int, 3>{}); break;
+        case 2: kloop(std::integral_constant<int, 2>{}); break;
+        case 1: kloop(std::integral_constant<int, 1>{}); break;
+        default: kloop(std::integral_constant<int, 0>{}); break;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // all loads landed, all reads done
+    if (cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= nvi) break;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; v += 4)
+                    stage4(p, smem, t, wm * 128 + i * 32 + r32, wn * 64 + j * 32 + 2 * v + 4 * h, p.N, acc[j][i][v],
+                           acc[j][i][v + 1], acc[j][i][v + 2], acc[j][i][v + 3]);
+        }
+    }
+    store_staged(p, smem, t, p.N);
+}
+
+template <bool ALIGNED>
+static hipError_t launch_mx_tile(const ProductArgs& p, hipStream_t s) {
+    const hipError_t e = allow_dynamic_lds<mx_tile_kernel<ALIGNED>>(kMxLds);
+    if (e != hipSuccess) return e;
+    const int64_t grid = tile_grid(p, (p.N + kTN - 1) / kTN);
+    hipLaunchKernelGGL((mx_tile_kernel<ALIGNED>), dim3((unsigned)grid), dim3(kTThreads), kMxLds, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s) {
+    const bool aligned = p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
+    return aligned ? launch_mx_tile<true>(p, s) : launch_mx_tile<false>(p, s);
+}
+
+}  // namespace moe

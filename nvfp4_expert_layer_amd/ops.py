@@ -11,7 +11,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _check, _ptrs, _stream, lib
+from . import _check, _stream, lib
 
 BF16, F16, F32, U8 = 0, 1, 2, 3
 _DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32, torch.uint8: U8}
@@ -55,33 +55,63 @@ def _lib():
     return _typed
 
 
+def _mismatch(t, name, dtypes, shape):
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected " + " or ".join(str(d) for d in dtypes))
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
 def _tensors(rows, dense):
-    """Checks the row tensors `rows` and the dense tensors `dense` (both: (tensor, name,
-    dtype or dtypes, shape); None passes as NULL) before any pointer is taken; returns
-    (pointer, row stride) of each row tensor, flattened, and the dense pointers."""
+    """Checks the row tensors `rows` (tensor, name, dtypes, shape) and the dense tensors
+    `dense` (tensor, name, dtype, shape), dtypes and shapes first; None passes as NULL.
+    Returns (pointer, row stride) of each row tensor, flattened, the dense pointers and
+    the device.  One pass with few attribute reads: small calls cost what this costs."""
+    out, ptrs, device, stray = [], [], None, None
     for t, name, dtypes, shape in rows:
         if t is None:
+            out += (None, 0)
             continue
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name}: dtype {t.dtype}, expected " + " or ".join(str(d) for d in dtypes))
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        if shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1:
+        if t.dtype not in dtypes or t.shape != shape:
+            _mismatch(t, name, dtypes, shape)
+        many, width = shape[0] > 1, shape[1]
+        step, inner = t.stride()
+        if inner != 1 and width > 1 and shape[0] > 0:
             raise ValueError(f"{name}: elements of a row must be contiguous (strides {t.stride()})")
-    ptrs = _ptrs(*dense)
-    out, cur = [], None
-    for t, name, _, shape in rows:
+        dev = t.get_device()
+        if device is None:
+            device = dev
+        if dev != device or dev < 0:
+            stray = stray or (t, name)
+        out += (t.data_ptr(), step if many else width)
+    for t, name, dtype, shape in dense:
         if t is None:
-            out += [None, 0]
+            ptrs.append(None)
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensor must be on the GPU")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.get_device() != cur:
-            raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{cur}")
-        out += [t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]]
-    return out, ptrs
+        if t.dtype is not dtype or t.shape != shape:
+            _mismatch(t, name, (dtype,), shape)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensor must be contiguous")
+        dev = t.get_device()
+        if device is None:
+            device = dev
+        if dev != device or dev < 0:
+            stray = stray or (t, name)
+        ptrs.append(t.data_ptr())
+    if stray is not None and not stray[0].is_cuda:
+        raise ValueError(f"{stray[1]}: tensor must be on the GPU")
+    # the library launches on the current device (and its stream)
+    cur = torch._C._cuda_getDevice()
+    if stray is not None or device != cur:
+        t, name = stray or next((t, n) for t, n, *_ in (*rows, *dense) if t is not None)
+        raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{cur}")
+    return out, ptrs, cur
+
+
+def _stream_of(stream, device):
+    """The raw handle of `stream`, by default the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
 # ------------------------------------------------------------ dispatch, combine
@@ -112,12 +142,13 @@ def moe_dispatch(problem, ids, x, counts, offsets, perm, inv, rows, workspace, s
     stay as they were.  Returns rows."""
     p, i32 = problem, torch.int32
     T, k, L, dt = p.num_tokens, p.top_k, p.num_local_experts, (_TORCH[p.dtype],)
-    (px, xs, pr, rs), (pi, pc, po, pp, pv, pw) = _tensors(
+    (px, xs, pr, rs), (pi, pc, po, pp, pv, pw), dev = _tensors(
         ((x, "x", dt, (T, p.width)), (rows, "rows", dt, (T * k, p.width))),
         ((ids, "ids", i32, (T, k)), (counts, "counts", i32, (L,)), (offsets, "offsets", i32, (L + 1,)),
-         (perm, "perm", i32, (T * k,)), (inv, "inv", i32, (T, k)), (workspace, "workspace", torch.uint8, (None,))))
+         (perm, "perm", i32, (T * k,)), (inv, "inv", i32, (T, k)),
+         (workspace, "workspace", torch.uint8, (workspace.numel(),))))
     _check(_lib().moe_dispatch(ctypes.byref(p), pi, px, xs, pc, po, pp, pv, pr, rs, pw, workspace.numel(),
-                               _stream(stream)))
+                               _stream_of(stream, dev)))
     return rows
 
 
@@ -125,9 +156,9 @@ def moe_dispatch_backward(problem, inv, drows, dx, stream=None):
     """dx [T, d] = the sum of each token's kept rows of drows [T k, d]."""
     p = problem
     T, k, dt = p.num_tokens, p.top_k, (_TORCH[p.dtype],)
-    (pr, rs, px, xs), (pv,) = _tensors(((drows, "drows", dt, (T * k, p.width)), (dx, "dx", dt, (T, p.width))),
+    (pr, rs, px, xs), (pv,), dev = _tensors(((drows, "drows", dt, (T * k, p.width)), (dx, "dx", dt, (T, p.width))),
                                        ((inv, "inv", torch.int32, (T, k)),))
-    _check(_lib().moe_dispatch_backward(ctypes.byref(p), pv, pr, rs, px, xs, _stream(stream)))
+    _check(_lib().moe_dispatch_backward(ctypes.byref(p), pv, pr, rs, px, xs, _stream_of(stream, dev)))
     return dx
 
 
@@ -135,10 +166,10 @@ def moe_combine(problem, inv, weights, rows, out, stream=None):
     """out [T, d] = each token's kept rows [T k, d] times weights fp32 [T, k], summed."""
     p = problem
     T, k, dt = p.num_tokens, p.top_k, (_TORCH[p.dtype],)
-    (pr, rs, po, os_), (pv, pw) = _tensors(
+    (pr, rs, po, os_), (pv, pw), dev = _tensors(
         ((rows, "rows", dt, (T * k, p.width)), (out, "out", dt, (T, p.width))),
         ((inv, "inv", torch.int32, (T, k)), (weights, "weights", torch.float32, (T, k))))
-    _check(_lib().moe_combine(ctypes.byref(p), pv, pw, pr, rs, po, os_, _stream(stream)))
+    _check(_lib().moe_combine(ctypes.byref(p), pv, pw, pr, rs, po, os_, _stream_of(stream, dev)))
     return out
 
 
@@ -148,11 +179,11 @@ def moe_combine_backward(problem, inv, weights, rows, dout, drows, dweights, str
     dweights).  Returns (drows, dweights)."""
     p = problem
     T, k, dt = p.num_tokens, p.top_k, (_TORCH[p.dtype],)
-    (pr, rs, po, os_, pg, gs), (pv, pw, pd) = _tensors(
+    (pr, rs, po, os_, pg, gs), (pv, pw, pd), dev = _tensors(
         ((rows, "rows", dt, (T * k, p.width)), (dout, "dout", dt, (T, p.width)), (drows, "drows", dt, (T * k, p.width))),
         ((inv, "inv", torch.int32, (T, k)), (weights, "weights", torch.float32, (T, k)),
          (dweights, "dweights", torch.float32, (T, k))))
-    _check(_lib().moe_combine_backward(ctypes.byref(p), pv, pw, pr, rs, po, os_, pg, gs, pd, _stream(stream)))
+    _check(_lib().moe_combine_backward(ctypes.byref(p), pv, pw, pr, rs, po, os_, pg, gs, pd, _stream_of(stream, dev)))
     return drows, dweights
 
 
@@ -196,8 +227,8 @@ def moe_mxfp4_quantize(x, codes, scales, stream=None):
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected (R, C)")
     R, C = x.shape
-    (px, xs), (pc, ps) = _tensors(((x, "x", _FLOATS, (R, C)),), _mx_specs(codes, scales, R, C))
-    _check(_lib().moe_mxfp4_quantize(px, _DTYPE[x.dtype], R, C, xs, pc, ps, _stream(stream)))
+    (px, xs), (pc, ps), dev = _tensors(((x, "x", _FLOATS, (R, C)),), _mx_specs(codes, scales, R, C))
+    _check(_lib().moe_mxfp4_quantize(px, _DTYPE[x.dtype], R, C, xs, pc, ps, _stream_of(stream, dev)))
     return codes, scales
 
 
@@ -207,8 +238,8 @@ def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     if out.dim() != 2:
         raise ValueError(f"out: shape {tuple(out.shape)}, expected (R, C)")
     R, C = out.shape
-    (po, os_), (pc, ps) = _tensors(((out, "out", _FLOATS, (R, C)),), _mx_specs(codes, scales, R, C))
-    _check(_lib().moe_mxfp4_dequantize(pc, ps, R, C, _DTYPE[out.dtype], po, os_, _stream(stream)))
+    (po, os_), (pc, ps), dev = _tensors(((out, "out", _FLOATS, (R, C)),), _mx_specs(codes, scales, R, C))
+    _check(_lib().moe_mxfp4_dequantize(pc, ps, R, C, _DTYPE[out.dtype], po, os_, _stream_of(stream, dev)))
     return out
 
 
@@ -221,7 +252,7 @@ def quantize_mxfp4_weights(w, out=None, start=0):
     if out is None:
         out, start = MXFP4Weights.empty(n, N, K, device=w.device), 0
     part = out.slice(start, n)
-    _ptrs(*_mx_specs(part.codes, part.scales, n, N, K, name="out."))
+    _tensors((), _mx_specs(part.codes, part.scales, n, N, K, name="out."))
     moe_mxfp4_quantize(w.view(n * N, K), part.codes.view(n * N, K // 2), part.scales.view(n * N, K // 32))
     return out
 
@@ -245,13 +276,13 @@ def moe_mxfp4_product(problem, a, w, offsets, out, stream=None):
     M, N, K = p.rows, p.n, p.k
     specs, rows = _weight_specs(p, w, offsets), ((out, "out", _FLOATS, (M, N)),)
     if isinstance(a, MXFP4Rows):
-        (po, os_), (pa, pas, pw, ps, pf) = _tensors(rows, (*_mx_specs(a.codes, a.scales, M, K, name="a."), *specs))
+        (po, os_), (pa, pas, pw, ps, pf), dev = _tensors(rows, (*_mx_specs(a.codes, a.scales, M, K, name="a."), *specs))
         as_ = K
     else:
-        (po, os_, pa, as_), (pw, ps, pf) = _tensors((*rows, (a, "a", (torch.bfloat16,), (M, K))), specs)
+        (po, os_, pa, as_), (pw, ps, pf), dev = _tensors((*rows, (a, "a", (torch.bfloat16,), (M, K))), specs)
         pas = None
     _check(_lib().moe_mxfp4_product(ctypes.byref(p), pa, pas, as_, pw, ps, pf, po, _DTYPE[out.dtype], os_,
-                                    _stream(stream)))
+                                    _stream_of(stream, dev)))
     return out
 
 
@@ -259,9 +290,9 @@ def moe_mxfp4_product_backward(problem, dout, w, offsets, drows, stream=None):
     """drows[r] = dout[r] . w[group of r] for the rows of every group; other rows stay
     as they were.  dout bfloat16 [M, N]; drows [M, K] (bfloat16, float16 or float32)."""
     p = problem
-    (pd, ds, po, os_), (pw, ps, pf) = _tensors(
+    (pd, ds, po, os_), (pw, ps, pf), dev = _tensors(
         ((dout, "dout", (torch.bfloat16,), (p.rows, p.n)), (drows, "drows", _FLOATS, (p.rows, p.k))),
         _weight_specs(p, w, offsets))
     _check(_lib().moe_mxfp4_product_backward(ctypes.byref(p), pd, ds, pw, ps, pf, po, _DTYPE[drows.dtype], os_,
-                                             _stream(stream)))
+                                             _stream_of(stream, dev)))
     return drows
