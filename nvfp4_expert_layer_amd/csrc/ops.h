@@ -73,5 +73,6 @@ struct ProductArgs {
 hipError_t launch_product(const ProductArgs& p, hipStream_t s);
 hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s);  // many rows a group
 hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s);   // a: dout bf16 [M][N]
+hipError_t launch_product_grad_tiles(const ProductArgs& p, hipStream_t s);
 
 }  // namespace moe

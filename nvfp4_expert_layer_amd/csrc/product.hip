@@ -234,12 +234,14 @@ hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
 }
 
 // Rows a group (an upper bound of their mean) up to which the weight is streamed.
-constexpr int kStreamRowsMx = 32;
+constexpr int kStreamRowsMx = 32, kStreamRowsBf16 = 32, kStreamRowsGrad = 32;
 
 hipError_t launch_product(const ProductArgs& p, hipStream_t s) {
-    const int64_t few = (int64_t)p.G * kStreamRowsMx;
-    return !p.a_s || p.M <= few ? launch_product_stream(p, s) : launch_product_tiles(p, s);
+    const int64_t few = (int64_t)p.G * (p.a_s ? kStreamRowsMx : kStreamRowsBf16);
+    return p.M <= few ? launch_product_stream(p, s) : launch_product_tiles(p, s);
 }
-hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s) { return launch_product_grad_stream(p, s); }
+hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s) {
+    return p.M <= (int64_t)p.G * kStreamRowsGrad ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, s);
+}
 
 }  // namespace moe

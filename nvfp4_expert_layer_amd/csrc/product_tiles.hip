@@ -305,18 +305,357 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     store_staged(p, smem, t, p.N);
 }
 
+// ---------------------------------------------------------------------------
+// W4A16
+// ---------------------------------------------------------------------------
+constexpr int kARows = 256 * 128;                        // 64 k of the tile's bf16 rows (32 KB)
+constexpr int kAChunk = kMxCodes + kMxScales;            // 128 k of the weight's codes and scales (17 KB)
+constexpr int kAOffW = 3 * kARows;                       // LDS: rows [3] | weight [3]
+constexpr int kALds = kAOffW + 3 * kAChunk;              // 147 KB
+
+__device__ __forceinline__ f32x16_t mfma_bf16_32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                   c, 0, 0, 0);
+}
+
 template <bool ALIGNED>
-static hipError_t launch_mx_tile(const ProductArgs& p, hipStream_t s) {
-    const hipError_t e = allow_dynamic_lds<mx_tile_kernel<ALIGNED>>(kMxLds);
+__global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const Tile t = find_tile(p, (p.N + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
+    if (t.g < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5;
+    const int wm = wave >> 2, wn = wave & 3;
+    // steps of 64 k, two to a weight chunk: an even number of them (the last may be
+    // all zeros)
+    const int KB = p.K / 32, nc = (KB + 3) / 4, nk = 2 * nc, n0 = t.nt * kTN;
+    auto wrow = [&](int r) { return (int64_t)t.g * p.N + min(n0 + r, p.N - 1); };
+
+    // rows: four loads of 1 KB (8 rows of 128 bytes) a wave and step; weight codes: two
+    // of 1 KB (16 rows of 64 bytes) a wave and chunk; scales: 64 rows' dwords, each
+    // quarter by two waves (the same bytes)
+    const uint16_t* asrc[4];
+    int au[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int r = (wave * 4 + q) * 8 + (lane >> 3);
+        au[q] = (lane & 7) ^ (lane >> 3) ^ (q & 1);
+        asrc[q] = static_cast<const uint16_t*>(p.a) + (int64_t)min(t.rb + r, t.re - 1) * p.as + au[q] * 8;
+    }
+    const uint8_t* csrc[2];
+    int cu[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = (wave * 2 + q) * 16 + (lane >> 2);
+        cu[q] = (lane & 3) ^ (((r >> 1) ^ (r >> 3)) & 3);
+        csrc[q] = p.w + wrow(r) * (p.K / 2) + cu[q] * 16;
+    }
+    const uint8_t* ssrc = p.w_s + wrow((wave & 3) * 64 + lane) * KB;
+
+    auto issue_rows = [&](int ks, int slot) {
+        uint8_t* base = smem + slot * kARows + wave * 4096;
+        const bool whole = ALIGNED || ks * 2 + 2 <= KB;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool in = whole || ks * 8 + au[q] < KB * 4;
+            to_lds16(in ? (const void*)(asrc[q] + (int64_t)ks * 64) : (const void*)kZeros, base + q * 1024);
+        }
+    };
+    auto issue_weight = [&](int c, int slot) {
+        uint8_t* base = smem + kAOffW + slot * kAChunk;
+        const bool whole = ALIGNED || c * 4 + 4 <= KB;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const bool in = whole || c * 4 + cu[q] < KB;
+            to_lds16(in ? csrc[q] + (int64_t)c * 64 : (const uint8_t*)kZeros, base + (wave * 2 + q) * 1024);
+        }
+        if (ALIGNED) to_lds4(ssrc + (int64_t)c * 4, base + kMxCodes + (wave & 3) * 256);
+    };
+    auto scale_bytes = [&](int c) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c * 4 + i < KB) v |= (uint32_t)ssrc[c * 4 + i] << (8 * i);
+        return v;
+    };
+    auto put_scales = [&](uint32_t v, int slot) {
+        *reinterpret_cast<uint32_t*>(smem + kAOffW + slot * kAChunk + kMxCodes + (wave & 3) * 256 + lane * 4) = v;
+    };
+
+    f32x16_t acc[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
+    const int nvi = max(0, min(4, (t.re - t.rb - wm * 128 + 31) >> 5));
+    const bool cols = n0 + wn * 64 < p.N;
+    const int r32 = lane & 31;
+
+    // Step ks: rows in slot ks % 3, chunk ks / 2 in weight slot (ks / 2) % 3.  Issued:
+    // the rows of step ks + 2 and, at even steps, chunk ks / 2 + 1 (past the end valid
+    // ones again).  The wait at the end leaves only this step's own loads in flight.
+    // Lane half h of MFMA kk takes k = 32 h + 8 kk .. + 8 of the step: dword kk of the
+    // weight row's unit 2 (ks % 2) + h, and the row's unit 4 h + kk.
+    auto step = [&](auto nv_c, auto st_c, int ks, int as, int ws) {
+        constexpr int NV = decltype(nv_c)::value;
+        constexpr int ST = decltype(st_c)::value;
+        issue_rows(min(ks + 2, nk - 1), as == 0 ? 2 : as - 1);
+        uint32_t pend = 0;
+        if (ST == 0) {
+            issue_weight(min(ks / 2 + 1, nc - 1), ws == 2 ? 0 : ws + 1);
+            if (!ALIGNED) pend = scale_bytes(min(ks / 2 + 1, nc - 1));
+        }
+        if constexpr (NV > 0) {
+            const uint8_t* A = smem + as * kARows;
+            const uint8_t* W = smem + kAOffW + ws * kAChunk;
+            u32x4_t wc[2];
+            float sc[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = wn * 64 + j * 32 + r32;
+                wc[j] = *reinterpret_cast<const u32x4_t*>(W + swz4(r, 2 * ST + h));
+                sc[j] = __uint_as_float((uint32_t)W[kMxCodes + r * 4 + 2 * ST + h] << 23);
+            }
+            u32x4_t av[2][4];
+            auto frag = [&](int kk, int f) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    av[f][i] = *reinterpret_cast<const u32x4_t*>(A + swz8(wm * 128 + i * 32 + r32, 4 * h + kk));
+            };
+            frag(0, 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                if (kk < 3) frag(kk + 1, (kk + 1) & 1);
+                u32x4_t wv[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[j][kk], sc[j]);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[kk & 1][i], acc[j][i]);
+            }
+        }
+        if (!ALIGNED) {
+            if (ST == 0) put_scales(pend, ws == 2 ? 0 : ws + 1);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        } else if (ST == 0) {
+            asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+    };
+    auto kloop = [&](auto nv_c) {
+        int as = 0, ws = 0;
+        for (int ks = 0; ks < nk; ks += 2) {
+            step(nv_c, std::integral_constant<int, 0>{}, ks, as, ws);
+            as = as == 2 ? 0 : as + 1;
+            step(nv_c, std::integral_constant<int, 1>{}, ks + 1, as, ws);
+            as = as == 2 ? 0 : as + 1;
+            ws = ws == 2 ? 0 : ws + 1;
+        }
+    };
+    issue_rows(0, 0);
+    issue_rows(1, 1);
+    issue_weight(0, 0);
+    if (!ALIGNED) put_scales(scale_bytes(0), 0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    switch (cols ? nvi : 0) {
+        case 4: kloop(std::integral_constant<int, 4>{}); break;
+        case 3: kloop(std::integral_constant<int, 3>{}); break;
+        case 2: kloop(std::integral_constant<int, 2>{}); break;
+        case 1: kloop(std::integral_constant<int, 1>{}); break;
+        default: kloop(std::integral_constant<int, 0>{}); break;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= nvi) break;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; v += 4)
+                    stage4(p, smem, t, wm * 128 + i * 32 + r32, wn * 64 + j * 32 + 2 * v + 4 * h, p.N, acc[j][i][v],
+                           acc[j][i][v + 1], acc[j][i][v + 2], acc[j][i][v + 3]);
+        }
+    }
+    store_staged(p, smem, t, p.N);
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+constexpr int kGDout = 256 * 128;                        // 64 n of the tile's bf16 gradient rows (32 KB)
+constexpr int kGCodes = 64 * 128;                        // 64 weight rows, 256 k (8 KB)
+constexpr int kGPitch = 144;                             // scales: [8 blocks][64 rows] as the upper halves of
+constexpr int kGScales = 8 * kGPitch;                    //   fp32 powers of two; the pitch spreads the banks
+constexpr int kGSlot = kGDout + kGCodes + kGScales;
+constexpr int kGLds = 3 * kGSlot;                        // 123 KB (the output's staging: 132 KB)
+constexpr int kGLdsAll = kGLds > kTM * kYS * 2 ? kGLds : kTM * kYS * 2;
+
+// VECTOR: dout's rows in 16-byte units (dout_vector), else element by element
+// through registers.
+template <bool VECTOR>
+__global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const Tile t = find_tile(p, (p.K + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
+    if (t.g < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r32 = lane & 31;
+    const int wt = wave >> 1, wk = wave & 1;             // rows 64 wt .. +64, columns 128 wk .. +128
+    const int KB = p.K / 32, kb0 = t.nt * 8, nn = (p.N + 63) / 64;
+
+    // dout: four loads of 8 rows a wave and stage; codes: one of 8 weight rows x 128
+    // bytes, whose two 64-byte halves trade places in every other group of 8 rows (the
+    // two lane halves read rows 8 apart: different banks); scales: one byte a thread
+    const uint16_t* dsrc[4];
+    int du[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int r = (wave * 4 + q) * 8 + (lane >> 3);
+        du[q] = (lane & 7) ^ (lane >> 3) ^ (q & 1);
+        dsrc[q] = static_cast<const uint16_t*>(p.a) + (int64_t)min(t.rb + r, t.re - 1) * p.as + du[q] * 8;
+    }
+    const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ ((wave & 1) << 2);
+    const bool cin = kb0 + cunit < KB;
+    const uint8_t* csrc = p.w + (int64_t)t.g * p.N * (p.K / 2) + (kb0 + cunit) * 16;
+    const int srow = tid >> 3, sblk = tid & 7;
+    const bool sin = kb0 + sblk < KB;
+    const uint8_t* ssrc = p.w_s + (int64_t)t.g * p.N * KB + min(kb0 + sblk, KB - 1);
+
+    auto issue = [&](int s, int slot) {
+        uint8_t* base = smem + slot * kGSlot;
+        if (VECTOR) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool in = s * 64 + du[q] * 8 < p.N;
+                to_lds16(in ? (const void*)(dsrc[q] + s * 64) : (const void*)kZeros, base + (wave * 4 + q) * 1024);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<u32x4_t*>(base + (wave * 4 + q) * 1024 + lane * 16) =
+                    load8_bf16<false>(dsrc[q] + s * 64, p.N - s * 64 - du[q] * 8);
+        }
+        const int n = s * 64 + crow;
+        to_lds16(cin && n < p.N ? csrc + (int64_t)n * (p.K / 2) : (const uint8_t*)kZeros,
+                 base + kGDout + wave * 1024);
+    };
+    // the byte is loaded from a valid place always and masked when it is stored: a
+    // branch around the load would wait for it at once
+    auto scale_byte = [&](int s) { return (uint32_t)ssrc[(int64_t)min(s * 64 + srow, p.N - 1) * KB]; };
+    auto put_scale = [&](uint32_t b, int s, int slot) {
+        *reinterpret_cast<uint16_t*>(smem + slot * kGSlot + kGDout + kGCodes + sblk * kGPitch + srow * 2) =
+            (uint16_t)(sin && s * 64 + srow < p.N ? b << 7 : 0u);
+    };
+
+    f32x16_t acc[4][2];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.f;
+    const int nvi = max(0, min(2, (t.re - t.rb - wt * 64 + 31) >> 5));
+    const bool cols = kb0 * 32 + wk * 128 < p.K;
+
+    // Stage s in slot s % 3, issued two ahead; its scales pass through a register, loaded
+    // before the stage's direct loads and stored to LDS at the step's end.  Lane half h of
+    // substep q (16 n) takes rows 16 q + 8 h .. + 8 of the stage.
+    auto nloop = [&](auto nv_c) {
+        constexpr int NV = decltype(nv_c)::value;
+        int slot = 0;
+        for (int s = 0; s < nn; ++s) {
+            const int ahead = slot == 0 ? 2 : slot - 1, sa = min(s + 2, nn - 1);
+            const uint32_t pend = scale_byte(sa);
+            issue(sa, ahead);
+            if constexpr (NV > 0) {
+                const uint8_t* D = smem + slot * kGSlot;
+                const uint8_t* C = D + kGDout + ((wk ^ h) * 64) + 2 * r32;
+                const uint8_t* S = D + kGDout + kGCodes + (wk * 4 + (r32 >> 3)) * kGPitch;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    u32x4_t dv[2];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        dv[i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 64 + i * 32 + r32, 2 * q + h));
+                    const u32x4_t sc = *reinterpret_cast<const u32x4_t*>(S + (16 * q + 8 * h) * 2);
+                    u32x4_t op[4];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const uint32_t c0 = *reinterpret_cast<const uint16_t*>(C + (16 * q + 8 * h + j) * 128);
+                        const uint32_t c1 = *reinterpret_cast<const uint16_t*>(C + (16 * q + 8 * h + j + 1) * 128);
+                        const float s0 = __uint_as_float(sc[j / 2] << 16), s1 = __uint_as_float(sc[j / 2] & 0xFFFF0000u);
+                        const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 0));
+                        const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 1));
+                        const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 0));
+                        const uint32_t b1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 1));
+                        op[0][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+                        op[1][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+                        op[2][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+                        op[3][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[i], acc[c][i]);
+                }
+            }
+            put_scale(pend, sa, ahead);
+            if (VECTOR) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            slot = slot == 2 ? 0 : slot + 1;
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        put_scale(scale_byte(min(s, nn - 1)), min(s, nn - 1), s);
+        issue(min(s, nn - 1), s);
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    switch (cols ? nvi : 0) {
+        case 2: nloop(std::integral_constant<int, 2>{}); break;
+        case 1: nloop(std::integral_constant<int, 1>{}); break;
+        default: nloop(std::integral_constant<int, 0>{}); break;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // operand row i of MFMA c holds column 4 i + c: value v of the four c are four
+    // consecutive columns
+    if (cols) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= nvi) break;
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                stage4(p, smem, t, wt * 64 + i * 32 + r32, wk * 128 + 4 * (8 * (v >> 2) + 4 * h + (v & 3)), p.K,
+                       acc[0][i][v], acc[1][i][v], acc[2][i][v], acc[3][i][v]);
+        }
+    }
+    store_staged(p, smem, t, p.K);
+}
+
+template <auto Kern, int LDS>
+static hipError_t launch_tiles(const ProductArgs& p, int width, hipStream_t s) {
+    const hipError_t e = allow_dynamic_lds<Kern>(LDS);
     if (e != hipSuccess) return e;
-    const int64_t grid = tile_grid(p, (p.N + kTN - 1) / kTN);
-    hipLaunchKernelGGL((mx_tile_kernel<ALIGNED>), dim3((unsigned)grid), dim3(kTThreads), kMxLds, s, p);
+    const int64_t grid = tile_grid(p, (width + kTN - 1) / kTN);
+    hipLaunchKernelGGL(Kern, dim3((unsigned)grid), dim3(kTThreads), LDS, s, p);
     return hipGetLastError();
 }
 
 hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s) {
-    const bool aligned = p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
-    return aligned ? launch_mx_tile<true>(p, s) : launch_mx_tile<false>(p, s);
+    const bool aligned =
+        p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
+    if (p.a_s)
+        return aligned ? launch_tiles<mx_tile_kernel<true>, kMxLds>(p, p.N, s)
+                       : launch_tiles<mx_tile_kernel<false>, kMxLds>(p, p.N, s);
+    return aligned ? launch_tiles<a16_tile_kernel<true>, kALds>(p, p.N, s)
+                   : launch_tiles<a16_tile_kernel<false>, kALds>(p, p.N, s);
+}
+
+hipError_t launch_product_grad_tiles(const ProductArgs& p, hipStream_t s) {
+    return dout_vector(p) ? launch_tiles<grad_tile_kernel<true>, kGLdsAll>(p, p.K, s)
+                          : launch_tiles<grad_tile_kernel<false>, kGLdsAll>(p, p.K, s);
 }
 
 }  // namespace moe
