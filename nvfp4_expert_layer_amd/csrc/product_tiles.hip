@@ -41,6 +41,17 @@ __device__ __forceinline__ void to_lds4(const void* src, void* dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 4, 0, 0);
 }
 
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
+}
+
+// p, or the zeros where `in` is false, without a branch (the compiler waits for every
+// outstanding load around one).
+__device__ __forceinline__ const void* within(bool in, const void* p) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), z = reinterpret_cast<uintptr_t>(kZeros);
+    return reinterpret_cast<const void*>(z ^ ((a ^ z) & (uintptr_t)-(intptr_t)in));
+}
+
 // Byte offset of 16-byte unit u of row r in a tile of 128-byte rows: eight
 // consecutive rows put a unit in eight different slots, rows r and r + 8 differ too.
 __device__ __forceinline__ int swz8(int r, int u) { return r * 128 + ((u ^ (r & 7) ^ ((r >> 3) & 1)) << 4); }
@@ -203,8 +214,8 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const bool in = whole || c * 4 + cu[q] < KB;
-            to_lds16(in ? csrc[q] + (int64_t)c * 64 : (const uint8_t*)kZeros, base + (wave * 2 + q) * 1024);
-            to_lds16(in ? asrc[q] + (int64_t)c * 64 : (const uint8_t*)kZeros, base + kMxCodes + (wave * 2 + q) * 1024);
+            to_lds16(within(in, csrc[q] + (int64_t)c * 64), base + (wave * 2 + q) * 1024);
+            to_lds16(within(in, asrc[q] + (int64_t)c * 64), base + kMxCodes + (wave * 2 + q) * 1024);
         }
         if (ALIGNED) to_lds4(ssrc + (int64_t)c * 4, base + sdst);
     };
@@ -357,7 +368,7 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const bool in = whole || ks * 8 + au[q] < KB * 4;
-            to_lds16(in ? (const void*)(asrc[q] + (int64_t)ks * 64) : (const void*)kZeros, base + q * 1024);
+            to_lds16(within(in, asrc[q] + (int64_t)ks * 64), base + q * 1024);
         }
     };
     auto issue_weight = [&](int c, int slot) {
@@ -366,7 +377,7 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const bool in = whole || c * 4 + cu[q] < KB;
-            to_lds16(in ? csrc[q] + (int64_t)c * 64 : (const uint8_t*)kZeros, base + (wave * 2 + q) * 1024);
+            to_lds16(within(in, csrc[q] + (int64_t)c * 64), base + (wave * 2 + q) * 1024);
         }
         if (ALIGNED) to_lds4(ssrc + (int64_t)c * 4, base + kMxCodes + (wave & 3) * 256);
     };
@@ -491,7 +502,8 @@ constexpr int kGCodes = 64 * 128;                        // 64 weight rows, 256 
 constexpr int kGPitch = 144;                             // scales: [8 blocks][64 rows] as the upper halves of
 constexpr int kGScales = 8 * kGPitch;                    //   fp32 powers of two; the pitch spreads the banks
 constexpr int kGSlot = kGDout + kGCodes + kGScales;
-constexpr int kGLds = 3 * kGSlot;                        // 123 KB (the output's staging: 132 KB)
+constexpr int kGOffRaw = 3 * kGSlot, kGRaw = 512 * 4;    // scale bytes as loaded, a dword each, three stages
+constexpr int kGLds = kGOffRaw + 3 * kGRaw;              // 130 KB (the output's staging: 132 KB)
 constexpr int kGLdsAll = kGLds > kTM * kYS * 2 ? kGLds : kTM * kYS * 2;
 
 // VECTOR: dout's rows in 16-byte units (dout_vector), else element by element
@@ -521,7 +533,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const uint8_t* csrc = p.w + (int64_t)t.g * p.N * (p.K / 2) + (kb0 + cunit) * 16;
     const int srow = tid >> 3, sblk = tid & 7;
     const bool sin = kb0 + sblk < KB;
-    const uint8_t* ssrc = p.w_s + (int64_t)t.g * p.N * KB + min(kb0 + sblk, KB - 1);
+    const uint8_t* ssrc = p.w_s + (int64_t)t.g * p.N * KB + kb0 + sblk;
 
     auto issue = [&](int s, int slot) {
         uint8_t* base = smem + slot * kGSlot;
@@ -529,7 +541,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const bool in = s * 64 + du[q] * 8 < p.N;
-                to_lds16(in ? (const void*)(dsrc[q] + s * 64) : (const void*)kZeros, base + (wave * 4 + q) * 1024);
+                to_lds16(within(in, dsrc[q] + s * 64), base + (wave * 4 + q) * 1024);
             }
         } else {
 #pragma unroll
@@ -538,15 +550,21 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
                     load8_bf16<false>(dsrc[q] + s * 64, p.N - s * 64 - du[q] * 8);
         }
         const int n = s * 64 + crow;
-        to_lds16(cin && n < p.N ? csrc + (int64_t)n * (p.K / 2) : (const uint8_t*)kZeros,
-                 base + kGDout + wave * 1024);
+        to_lds16(within(cin && n < p.N, csrc + (int64_t)n * (p.K / 2)), base + kGDout + wave * 1024);
     };
-    // the byte is loaded from a valid place always and masked when it is stored: a
-    // branch around the load would wait for it at once
-    auto scale_byte = [&](int s) { return (uint32_t)ssrc[(int64_t)min(s * 64 + srow, p.N - 1) * KB]; };
-    auto put_scale = [&](uint32_t b, int s, int slot) {
-        *reinterpret_cast<uint16_t*>(smem + slot * kGSlot + kGDout + kGCodes + sblk * kGPitch + srow * 2) =
-            (uint16_t)(sin && s * 64 + srow < p.N ? b << 7 : 0u);
+    // scales: byte tid of a stage (row tid / 8, block tid % 8) to a dword of its own
+    auto issue_scales = [&](int s, int slot) {
+        const int n = s * 64 + srow;
+        __builtin_amdgcn_global_load_lds(within(sin && n < p.N, ssrc + (int64_t)n * KB),
+                                         (lds_void_t*)(smem + kGOffRaw + slot * kGRaw + wave * 256), 1, 0, 0);
+    };
+    // and from there, a stage later, to where the operands are decoded
+    auto put_scales = [&](int slot) {
+        const uint32_t b = smem[kGOffRaw + slot * kGRaw + tid * 4];
+        const uint32_t at = lds_offset(smem) + slot * kGSlot + kGDout + kGCodes + sblk * kGPitch + srow * 2;
+        // written out: before an ordinary LDS store the compiler waits for every direct
+        // load in flight (they write LDS too).  The step's own wait covers it.
+        asm volatile("ds_write_b16 %0, %1" ::"v"(at), "v"(b << 7) : "memory");
     };
 
     f32x16_t acc[4][2];
@@ -559,16 +577,17 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const int nvi = max(0, min(2, (t.re - t.rb - wt * 64 + 31) >> 5));
     const bool cols = kb0 * 32 + wk * 128 < p.K;
 
-    // Stage s in slot s % 3, issued two ahead; its scales pass through a register, loaded
-    // before the stage's direct loads and stored to LDS at the step's end.  Lane half h of
-    // substep q (16 n) takes rows 16 q + 8 h .. + 8 of the stage.
+    // Stage s in slot s % 3, issued two ahead, its scales three ahead: they have landed
+    // one step before the others and are rearranged then.  Lane half h of substep q
+    // (16 n) takes rows 16 q + 8 h .. + 8 of the stage.
     auto nloop = [&](auto nv_c) {
         constexpr int NV = decltype(nv_c)::value;
         int slot = 0;
         for (int s = 0; s < nn; ++s) {
-            const int ahead = slot == 0 ? 2 : slot - 1, sa = min(s + 2, nn - 1);
-            const uint32_t pend = scale_byte(sa);
-            issue(sa, ahead);
+            const int next = slot == 2 ? 0 : slot + 1, ahead = slot == 0 ? 2 : slot - 1;
+            issue(min(s + 2, nn - 1), ahead);
+            issue_scales(min(s + 3, nn - 1), slot);
+            put_scales(next);
             if constexpr (NV > 0) {
                 const uint8_t* D = smem + slot * kGSlot;
                 const uint8_t* C = D + kGDout + ((wk ^ h) * 64) + 2 * r32;
@@ -601,17 +620,18 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
                         for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[i], acc[c][i]);
                 }
             }
-            put_scale(pend, sa, ahead);
-            if (VECTOR) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            slot = slot == 2 ? 0 : slot + 1;
+            if (VECTOR) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            slot = next;
         }
     };
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        put_scale(scale_byte(min(s, nn - 1)), min(s, nn - 1), s);
-        issue(min(s, nn - 1), s);
+    for (int s = 0; s < 3; ++s) {
+        if (s < 2) issue(min(s, nn - 1), s);
+        issue_scales(min(s, nn - 1), s);
     }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    put_scales(0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
         case 2: nloop(std::integral_constant<int, 2>{}); break;
