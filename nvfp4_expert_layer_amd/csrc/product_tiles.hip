@@ -40,6 +40,20 @@ __device__ __forceinline__ void to_lds16(const void* src, void* dst) {
 __device__ __forceinline__ void to_lds4(const void* src, void* dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 4, 0, 0);
 }
+// one byte a lane, each to a dword of its own
+__device__ __forceinline__ void to_lds1(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 1, 0, 0);
+}
+// A wave-uniform pointer, in scalar registers and opaque: loads then take it with a
+// 32-bit lane offset (else each load keeps and advances a 64-bit pointer a lane).
+template <typename T>
+__device__ __forceinline__ T* scalar(T* p) {
+    asm("" : "+s"(p));
+    return p;
+}
+// Operand reads stay before the MFMAs that follow them in the source (the scheduler
+// would sink each read to its use and wait for it there).
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
@@ -110,7 +124,10 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& p, int NT, int* s) 
     }
     __syncthreads();
     Tile t{-1, 0, 0, 0};
-    if (live) t = Tile{s[8], s[9], s[10], (int)(logical - (int64_t)tile * NT)};
+    // scalar registers: the addresses below are a scalar base and a 32-bit lane offset
+    if (live)
+        t = Tile{__builtin_amdgcn_readfirstlane(s[8]), __builtin_amdgcn_readfirstlane(s[9]),
+                 __builtin_amdgcn_readfirstlane(s[10]), (int)(logical - (int64_t)tile * NT)};
     __syncthreads();                                     // s is free again
     return t;
 }
@@ -166,9 +183,12 @@ __device__ __forceinline__ void store_staged(const ProductArgs& p, const uint8_t
 // W4A4
 // ---------------------------------------------------------------------------
 constexpr int kMxStages = 4;
-constexpr int kMxCodes = 256 * 64, kMxScales = 256 * 4;     // an operand's 128 k of a stage
-constexpr int kMxSlot = 2 * kMxCodes + 2 * kMxScales;       // weight codes | row codes | weight scales | row scales
-constexpr int kMxLds = kMxStages * kMxSlot;                 // 136 KB
+constexpr int kMxCodes = 256 * 64;                          // an operand's 128 k of a stage
+// its scales: a row's four bytes in one dword, or (rows not aligned to dwords) each in
+// one of its own, [4 blocks][256 rows]
+constexpr int mx_scales(bool aligned) { return aligned ? 256 * 4 : 256 * 16; }
+constexpr int mx_slot(bool aligned) { return 2 * kMxCodes + 2 * mx_scales(aligned); }   // codes: weight | rows; scales
+constexpr int mx_lds(bool aligned) { return kMxStages * mx_slot(aligned); }             // 136 or 160 KB
 
 template <int OPSEL>
 __device__ __forceinline__ f32x16_t mfma_mx32(const u32x4_t& a, uint32_t as, const u32x4_t& b, uint32_t bs,
@@ -180,55 +200,64 @@ __device__ __forceinline__ f32x16_t mfma_mx32(const u32x4_t& a, uint32_t as, con
 // ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales).
 template <bool ALIGNED>
 __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
+    constexpr int kMxScales = mx_scales(ALIGNED), kMxSlot = mx_slot(ALIGNED);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const Tile t = find_tile(p, (p.N + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
     if (t.g < 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int wm = wave >> 2, wn = wave & 3;             // rows 128 wm .. +128, outputs 64 wn .. +64
     const int KB = p.K / 32, nc = (KB + 3) / 4, n0 = t.nt * kTN;
-    const uint8_t* acodes = static_cast<const uint8_t*>(p.a);
+    const int64_t w0 = (int64_t)t.g * p.N + n0;
+    const uint8_t* wbase = p.w + w0 * (p.K / 2);
+    const uint8_t* abase = static_cast<const uint8_t*>(p.a) + (int64_t)t.rb * (p.K / 2);
     // rows and outputs past the tile's end: any valid row (their results are not stored)
-    auto arow = [&](int r) { return (int64_t)min(t.rb + r, t.re - 1); };
-    auto wrow = [&](int r) { return (int64_t)t.g * p.N + min(n0 + r, p.N - 1); };
+    auto arow = [&](int r) { return (uint32_t)min(r, t.re - 1 - t.rb); };
+    auto wrow = [&](int r) { return (uint32_t)min(r, p.N - 1 - n0); };
 
     // loads of a stage: per operand 16 KB of codes, two of 1 KB a wave: load q of wave w
     // fills rows 16 (2 w + q) .. +16, lane i row i / 4, slot i % 4, which holds unit
     // (i % 4) ^ f(row) of the stage (swz4); scales: 256 bytes a wave, waves 0-3 the
     // weight's rows 64 w .. +64, waves 4-7 the rows'
-    const uint8_t *csrc[2], *asrc[2];
+    uint32_t coff[2], aoff[2];
     int cu[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int r = (wave * 2 + q) * 16 + (lane >> 2);
         cu[q] = (lane & 3) ^ (((r >> 1) ^ (r >> 3)) & 3);
-        csrc[q] = p.w + wrow(r) * (p.K / 2) + cu[q] * 16;
-        asrc[q] = acodes + arow(r) * (p.K / 2) + cu[q] * 16;
+        coff[q] = wrow(r) * (uint32_t)(p.K / 2) + cu[q] * 16;
+        aoff[q] = arow(r) * (uint32_t)(p.K / 2) + cu[q] * 16;
     }
     const int srow = (wave & 3) * 64 + lane;
-    const uint8_t* ssrc = wave < 4 ? p.w_s + wrow(srow) * KB : p.a_s + arow(srow) * KB;
+    const uint8_t* sbase = wave < 4 ? p.w_s + w0 * KB : p.a_s + (int64_t)t.rb * KB;
+    const uint32_t soff = (wave < 4 ? wrow(srow) : arow(srow)) * (uint32_t)KB;
     const int sdst = 2 * kMxCodes + (wave < 4 ? 0 : kMxScales) + (wave & 3) * 256;
 
     auto issue = [&](int c, int slot) {
-        uint8_t* base = smem + slot * kMxSlot;
-        const bool whole = ALIGNED || c * 4 + 4 <= KB;
+        uint8_t* base = smem + slot * kMxSlot + wave * 2048;
+        const uint8_t *wb = scalar(wbase + (int64_t)c * 64), *ab = scalar(abase + (int64_t)c * 64);
+        if (ALIGNED || c * 4 + 4 <= KB) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const bool in = whole || c * 4 + cu[q] < KB;
-            to_lds16(within(in, csrc[q] + (int64_t)c * 64), base + (wave * 2 + q) * 1024);
-            to_lds16(within(in, asrc[q] + (int64_t)c * 64), base + kMxCodes + (wave * 2 + q) * 1024);
+            for (int q = 0; q < 2; ++q) {
+                to_lds16(wb + coff[q], base + q * 1024);
+                to_lds16(ab + aoff[q], base + kMxCodes + q * 1024);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const bool in = c * 4 + cu[q] < KB;
+                to_lds16(within(in, wb + coff[q]), base + q * 1024);
+                to_lds16(within(in, ab + aoff[q]), base + kMxCodes + q * 1024);
+            }
         }
-        if (ALIGNED) to_lds4(ssrc + (int64_t)c * 4, base + sdst);
-    };
-    // unaligned scale rows: bytes through a register
-    auto scale_bytes = [&](int c) {
-        uint32_t v = 0;
+        uint8_t* sd = smem + slot * kMxSlot + sdst;
+        const uint8_t* sb = scalar(sbase + (int64_t)c * 4);
+        if (ALIGNED) {
+            to_lds4(sb + soff, sd);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c * 4 + i < KB) v |= (uint32_t)ssrc[c * 4 + i] << (8 * i);
-        return v;
-    };
-    auto put_scales = [&](uint32_t v, int slot) {
-        *reinterpret_cast<uint32_t*>(smem + slot * kMxSlot + sdst + lane * 4) = v;
+            for (int i = 0; i < 4; ++i)
+                to_lds1(within(c * 4 + i < KB, sb + i + soff), sd + i * 1024);
+        }
     };
 
     f32x16_t acc[2][4];
@@ -242,56 +271,80 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     const bool cols = n0 + wn * 64 < p.N;
     const int r32 = lane & 31;
 
-    // Stage c sits in slot c % 4 and is three stages ahead when issued, into the slot
-    // that the last barrier freed; past the end valid stages are loaded again, so each
-    // step issues the same five loads and the wait leaves the two newer stages in
-    // flight.  Lane half h of MFMA m takes block 2 h + m of the stage's four.
+    // Stage c sits in slot c % 4.  Lane half h of its MFMA m (0, 1) takes block 2 h + m of
+    // the stage's four.  A step's second operands are read before its first MFMAs, the
+    // next stage's first ones before its second MFMAs, so that the matrix cores do not
+    // wait for LDS; the barrier stands between the two, where the step's slot has been
+    // read and stage c + 4 may take it.  Past the end valid stages are loaded again, so
+    // that each step issues as many loads and the wait leaves the two newer stages in flight.
     auto kloop = [&](auto nv_c) {
         constexpr int NV = decltype(nv_c)::value;
-        for (int c = 0; c < nc; ++c) {
-            issue(min(c + 3, nc - 1), (c + 3) & 3);
-            uint32_t pend = 0;
-            if (!ALIGNED && c + 1 < nc) pend = scale_bytes(c + 1);
+        u32x4_t wv[2][2], av[2][4];
+        uint32_t ws[2][2], as[2][4];                      // scales by parity of the stage
+        auto operands = [&](int c, auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            const uint8_t* S = smem + (c & 3) * kMxSlot;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                wv[m][j] = *reinterpret_cast<const u32x4_t*>(S + swz4(wn * 64 + j * 32 + r32, 2 * h + m));
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                av[m][i] = *reinterpret_cast<const u32x4_t*>(S + kMxCodes + swz4(wm * 128 + i * 32 + r32, 2 * h + m));
+        };
+        auto scale_pair = [&](const uint8_t* S, int r) {       // blocks 2 h and 2 h + 1 of row r
+            if (ALIGNED) return (uint32_t)*reinterpret_cast<const uint16_t*>(S + r * 4 + 2 * h);
+            return *reinterpret_cast<const uint32_t*>(S + 2048 * h + r * 4) |
+                   (*reinterpret_cast<const uint32_t*>(S + 2048 * h + 1024 + r * 4) << 8);
+        };
+        auto scales = [&](int c, auto f_c) {
+            constexpr int f = decltype(f_c)::value;
+            const uint8_t* S = smem + (c & 3) * kMxSlot + 2 * kMxCodes;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) ws[f][j] = scale_pair(S, wn * 64 + j * 32 + r32);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) as[f][i] = scale_pair(S + kMxScales, wm * 128 + i * 32 + r32);
+        };
+        const std::integral_constant<int, 0> c0;
+        const std::integral_constant<int, 1> c1;
+        auto stage = [&](int c, auto f_c, auto g_c) {
+            constexpr int f = decltype(f_c)::value;
             if constexpr (NV > 0) {
-                const uint8_t* S = smem + (c & 3) * kMxSlot;
-                uint32_t ws[2], as[4];
-                u32x4_t wv[2][2], av[2][4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = wn * 64 + j * 32 + r32;
-                    ws[j] = *reinterpret_cast<const uint32_t*>(S + 2 * kMxCodes + r * 4) >> (16 * h);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) wv[m][j] = *reinterpret_cast<const u32x4_t*>(S + swz4(r, 2 * h + m));
-                }
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int r = wm * 128 + i * 32 + r32;
-                    as[i] = *reinterpret_cast<const uint32_t*>(S + 2 * kMxCodes + kMxScales + r * 4) >> (16 * h);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-                        av[m][i] = *reinterpret_cast<const u32x4_t*>(S + kMxCodes + swz4(r, 2 * h + m));
-                }
+                operands(c, c1);
+                keep_order();
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_mx32<0>(wv[0][j], ws[j], av[0][i], as[i], acc[j][i]);
+                    for (int j = 0; j < 2; ++j)
+                        acc[j][i] = mfma_mx32<0>(wv[0][j], ws[f][j], av[0][i], as[f][i], acc[j][i]);
+            }
+            keep_order();
+            if (ALIGNED) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue(min(c + 4, nc - 1), c & 3);
+            if constexpr (NV > 0) {
+                operands(c + 1, c0);
+                scales(c + 1, g_c);
+                keep_order();
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_mx32<1>(wv[1][j], ws[j], av[1][i], as[i], acc[j][i]);
+                    for (int j = 0; j < 2; ++j)
+                        acc[j][i] = mfma_mx32<1>(wv[1][j], ws[f][j], av[1][i], as[f][i], acc[j][i]);
             }
-            if (ALIGNED) {
-                asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            } else {
-                put_scales(pend, (c + 1) & 3);
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            }
+        };
+        if constexpr (NV > 0) {
+            operands(0, c0);
+            scales(0, c0);
         }
+        int c = 0;
+        for (; c + 1 < nc; c += 2) {
+            stage(c, c0, c1);
+            stage(c + 1, c1, c0);
+        }
+        if (c < nc) stage(c, c0, c1);
     };
-    issue(0, 0);
-    issue(min(1, nc - 1), 1);
-    issue(min(2, nc - 1), 2);
-    if (!ALIGNED) put_scales(scale_bytes(0), 0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) issue(min(c, nc - 1), c);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
         case 4: kloop(std::integral_constant<int, 4>{}); break;
@@ -320,9 +373,9 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
 // W4A16
 // ---------------------------------------------------------------------------
 constexpr int kARows = 256 * 128;                        // 64 k of the tile's bf16 rows (32 KB)
-constexpr int kAChunk = kMxCodes + kMxScales;            // 128 k of the weight's codes and scales (17 KB)
+constexpr int a16_chunk(bool aligned) { return kMxCodes + mx_scales(aligned); }   // 128 k of the weight
 constexpr int kAOffW = 3 * kARows;                       // LDS: rows [3] | weight [3]
-constexpr int kALds = kAOffW + 3 * kAChunk;              // 147 KB
+constexpr int a16_lds(bool aligned) { return kAOffW + 3 * a16_chunk(aligned); }   // 147 or 156 KB
 
 __device__ __forceinline__ f32x16_t mfma_bf16_32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
@@ -331,65 +384,74 @@ __device__ __forceinline__ f32x16_t mfma_bf16_32(const u32x4_t& a, const u32x4_t
 
 template <bool ALIGNED>
 __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
+    constexpr int kAChunk = a16_chunk(ALIGNED);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const Tile t = find_tile(p, (p.N + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
     if (t.g < 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int wm = wave >> 2, wn = wave & 3;
     // steps of 64 k, two to a weight chunk: an even number of them (the last may be
     // all zeros)
     const int KB = p.K / 32, nc = (KB + 3) / 4, nk = 2 * nc, n0 = t.nt * kTN;
-    auto wrow = [&](int r) { return (int64_t)t.g * p.N + min(n0 + r, p.N - 1); };
+    const int64_t w0 = (int64_t)t.g * p.N + n0;
+    const uint8_t* wbase = p.w + w0 * (p.K / 2);
+    const uint8_t* sbase = p.w_s + w0 * KB;
+    const uint16_t* abase = static_cast<const uint16_t*>(p.a) + (int64_t)t.rb * p.as;
+    auto wrow = [&](int r) { return (uint32_t)min(r, p.N - 1 - n0); };
 
     // rows: four loads of 1 KB (8 rows of 128 bytes) a wave and step; weight codes: two
     // of 1 KB (16 rows of 64 bytes) a wave and chunk; scales: 64 rows' dwords, each
-    // quarter by two waves (the same bytes)
-    const uint16_t* asrc[4];
+    // quarter by two waves (the same bytes), or two of a row's four bytes a wave
+    uint32_t aoff[4];
     int au[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int r = (wave * 4 + q) * 8 + (lane >> 3);
         au[q] = (lane & 7) ^ (lane >> 3) ^ (q & 1);
-        asrc[q] = static_cast<const uint16_t*>(p.a) + (int64_t)min(t.rb + r, t.re - 1) * p.as + au[q] * 8;
+        aoff[q] = (uint32_t)(min(r, t.re - 1 - t.rb) * p.as + au[q] * 8);
     }
-    const uint8_t* csrc[2];
+    uint32_t coff[2];
     int cu[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int r = (wave * 2 + q) * 16 + (lane >> 2);
         cu[q] = (lane & 3) ^ (((r >> 1) ^ (r >> 3)) & 3);
-        csrc[q] = p.w + wrow(r) * (p.K / 2) + cu[q] * 16;
+        coff[q] = wrow(r) * (uint32_t)(p.K / 2) + cu[q] * 16;
     }
-    const uint8_t* ssrc = p.w_s + wrow((wave & 3) * 64 + lane) * KB;
+    const uint32_t soff = wrow((wave & 3) * 64 + lane) * (uint32_t)KB;
 
     auto issue_rows = [&](int ks, int slot) {
         uint8_t* base = smem + slot * kARows + wave * 4096;
-        const bool whole = ALIGNED || ks * 2 + 2 <= KB;
+        const uint16_t* ab = scalar(abase + (int64_t)ks * 64);
+        if (ALIGNED || ks * 2 + 2 <= KB) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const bool in = whole || ks * 8 + au[q] < KB * 4;
-            to_lds16(within(in, asrc[q] + (int64_t)ks * 64), base + q * 1024);
+            for (int q = 0; q < 4; ++q) to_lds16(ab + aoff[q], base + q * 1024);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) to_lds16(within(ks * 8 + au[q] < KB * 4, ab + aoff[q]), base + q * 1024);
         }
     };
     auto issue_weight = [&](int c, int slot) {
         uint8_t* base = smem + kAOffW + slot * kAChunk;
-        const bool whole = ALIGNED || c * 4 + 4 <= KB;
+        const uint8_t *wb = scalar(wbase + (int64_t)c * 64), *sb = scalar(sbase + (int64_t)c * 4);
+        if (ALIGNED || c * 4 + 4 <= KB) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const bool in = whole || c * 4 + cu[q] < KB;
-            to_lds16(within(in, csrc[q] + (int64_t)c * 64), base + (wave * 2 + q) * 1024);
+            for (int q = 0; q < 2; ++q) to_lds16(wb + coff[q], base + (wave * 2 + q) * 1024);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                to_lds16(within(c * 4 + cu[q] < KB, wb + coff[q]), base + (wave * 2 + q) * 1024);
         }
-        if (ALIGNED) to_lds4(ssrc + (int64_t)c * 4, base + kMxCodes + (wave & 3) * 256);
-    };
-    auto scale_bytes = [&](int c) {
-        uint32_t v = 0;
+        if (ALIGNED) {
+            to_lds4(sb + soff, base + kMxCodes + (wave & 3) * 256);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c * 4 + i < KB) v |= (uint32_t)ssrc[c * 4 + i] << (8 * i);
-        return v;
-    };
-    auto put_scales = [&](uint32_t v, int slot) {
-        *reinterpret_cast<uint32_t*>(smem + kAOffW + slot * kAChunk + kMxCodes + (wave & 3) * 256 + lane * 4) = v;
+            for (int i = 0; i < 2; ++i) {
+                const int b = (wave >> 2) * 2 + i;
+                to_lds1(within(c * 4 + b < KB, sb + b + soff),
+                        base + kMxCodes + b * 1024 + (wave & 3) * 256);
+            }
+        }
     };
 
     f32x16_t acc[2][4];
@@ -403,73 +465,90 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     const bool cols = n0 + wn * 64 < p.N;
     const int r32 = lane & 31;
 
-    // Step ks: rows in slot ks % 3, chunk ks / 2 in weight slot (ks / 2) % 3.  Issued:
-    // the rows of step ks + 2 and, at even steps, chunk ks / 2 + 1 (past the end valid
-    // ones again).  The wait at the end leaves only this step's own loads in flight.
-    // Lane half h of MFMA kk takes k = 32 h + 8 kk .. + 8 of the step: dword kk of the
-    // weight row's unit 2 (ks % 2) + h, and the row's unit 4 h + kk.
-    auto step = [&](auto nv_c, auto st_c, int ks, int as, int ws) {
+    // Step ks: rows in slot ks % 3, chunk ks / 2 in weight slot (ks / 2) % 3.  Lane half h
+    // of MFMA kk (0 .. 3) takes k = 32 h + 8 kk .. + 8 of the step: dword kk of the weight
+    // row's unit 2 (ks % 2) + h, and the row's unit 4 h + kk.  Operands are read one MFMA
+    // ahead, a step's first ones before the last MFMAs of the step before.  The barrier
+    // stands there: the step's rows have been read (slot free for step ks + 3), after an
+    // odd step its chunk too (for chunk + 3), and the wait leaves in flight only what was
+    // issued since the next step's rows (past the end valid data again).
+    auto kloop = [&](auto nv_c) {
         constexpr int NV = decltype(nv_c)::value;
-        constexpr int ST = decltype(st_c)::value;
-        issue_rows(min(ks + 2, nk - 1), as == 0 ? 2 : as - 1);
-        uint32_t pend = 0;
-        if (ST == 0) {
-            issue_weight(min(ks / 2 + 1, nc - 1), ws == 2 ? 0 : ws + 1);
-            if (!ALIGNED) pend = scale_bytes(min(ks / 2 + 1, nc - 1));
-        }
-        if constexpr (NV > 0) {
-            const uint8_t* A = smem + as * kARows;
-            const uint8_t* W = smem + kAOffW + ws * kAChunk;
-            u32x4_t wc[2];
-            float sc[2];
+        u32x4_t wc[2][2], av[2][4];                       // codes by parity of the step; rows by parity of kk
+        float sc[2][2];
+        int as = 0, ws = 0;
+        auto rows = [&](int slot, int kk, auto f_c) {
+            constexpr int f = decltype(f_c)::value;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                av[f][i] = *reinterpret_cast<const u32x4_t*>(smem + slot * kARows +
+                                                             swz8(wm * 128 + i * 32 + r32, 4 * h + kk));
+        };
+        auto codes = [&](int slot, auto st_c) {
+            constexpr int ST = decltype(st_c)::value;
+            const uint8_t* W = smem + kAOffW + slot * kAChunk;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int r = wn * 64 + j * 32 + r32;
-                wc[j] = *reinterpret_cast<const u32x4_t*>(W + swz4(r, 2 * ST + h));
-                sc[j] = __uint_as_float((uint32_t)W[kMxCodes + r * 4 + 2 * ST + h] << 23);
+                const int r = wn * 64 + j * 32 + r32, b = 2 * ST + h;
+                wc[ST][j] = *reinterpret_cast<const u32x4_t*>(W + swz4(r, b));
+                const uint32_t sb = W[kMxCodes + (ALIGNED ? r * 4 + b : b * 1024 + r * 4)];
+                sc[ST][j] = __uint_as_float(sb << 23);
             }
-            u32x4_t av[2][4];
-            auto frag = [&](int kk, int f) {
+        };
+        auto mfmas = [&](auto st_c, int kk, auto f_c) {
+            constexpr int ST = decltype(st_c)::value, f = decltype(f_c)::value;
+            u32x4_t wv[2];
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    av[f][i] = *reinterpret_cast<const u32x4_t*>(A + swz8(wm * 128 + i * 32 + r32, 4 * h + kk));
-            };
-            frag(0, 0);
+            for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[ST][j][kk], sc[ST][j]);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                if (kk < 3) frag(kk + 1, (kk + 1) & 1);
-                u32x4_t wv[2];
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[j][kk], sc[j]);
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[kk & 1][i], acc[j][i]);
+                for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[f][i], acc[j][i]);
+        };
+        const std::integral_constant<int, 0> c0;
+        const std::integral_constant<int, 1> c1;
+        auto step = [&](int ks, auto st_c, auto next_c) {
+            constexpr int ST = decltype(st_c)::value;
+            const int an = as == 2 ? 0 : as + 1, wnx = ws == 2 ? 0 : ws + 1;
+            if constexpr (NV > 0) {
+                rows(as, 1, c1);
+                keep_order();
+                mfmas(st_c, 0, c0);
+                rows(as, 2, c0);
+                keep_order();
+                mfmas(st_c, 1, c1);
+                rows(as, 3, c1);
+                keep_order();
+                mfmas(st_c, 2, c0);
             }
+            keep_order();
+            if (ALIGNED) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue_rows(min(ks + 3, nk - 1), as);
+            if (ST == 1) issue_weight(min(ks / 2 + 3, nc - 1), ws);
+            if constexpr (NV > 0) {
+                codes(ST == 1 ? wnx : ws, next_c);
+                rows(an, 0, c0);
+                keep_order();
+                mfmas(st_c, 3, c1);
+            }
+            as = an;
+            if (ST == 1) ws = wnx;
+        };
+        if constexpr (NV > 0) {
+            codes(0, c0);
+            rows(0, 0, c0);
         }
-        if (!ALIGNED) {
-            if (ST == 0) put_scales(pend, ws == 2 ? 0 : ws + 1);
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        } else if (ST == 0) {
-            asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        } else {
-            asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        }
-    };
-    auto kloop = [&](auto nv_c) {
-        int as = 0, ws = 0;
         for (int ks = 0; ks < nk; ks += 2) {
-            step(nv_c, std::integral_constant<int, 0>{}, ks, as, ws);
-            as = as == 2 ? 0 : as + 1;
-            step(nv_c, std::integral_constant<int, 1>{}, ks + 1, as, ws);
-            as = as == 2 ? 0 : as + 1;
-            ws = ws == 2 ? 0 : ws + 1;
+            step(ks, c0, c1);
+            step(ks + 1, c1, c0);
         }
     };
-    issue_rows(0, 0);
-    issue_rows(1, 1);
-    issue_weight(0, 0);
-    if (!ALIGNED) put_scales(scale_bytes(0), 0);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        issue_rows(min(i, nk - 1), i);
+        issue_weight(min(i, nc - 1), i);
+    }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
         case 4: kloop(std::integral_constant<int, 4>{}); break;
@@ -513,52 +592,61 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const Tile t = find_tile(p, (p.K + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
     if (t.g < 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r32 = lane & 31;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int r32 = lane & 31;
     const int wt = wave >> 1, wk = wave & 1;             // rows 64 wt .. +64, columns 128 wk .. +128
     const int KB = p.K / 32, kb0 = t.nt * 8, nn = (p.N + 63) / 64;
 
     // dout: four loads of 8 rows a wave and stage; codes: one of 8 weight rows x 128
     // bytes, whose two 64-byte halves trade places in every other group of 8 rows (the
     // two lane halves read rows 8 apart: different banks); scales: one byte a thread
-    const uint16_t* dsrc[4];
+    const uint16_t* dbase = static_cast<const uint16_t*>(p.a) + (int64_t)t.rb * p.as;
+    uint32_t doff[4];
     int du[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int r = (wave * 4 + q) * 8 + (lane >> 3);
         du[q] = (lane & 7) ^ (lane >> 3) ^ (q & 1);
-        dsrc[q] = static_cast<const uint16_t*>(p.a) + (int64_t)min(t.rb + r, t.re - 1) * p.as + du[q] * 8;
+        doff[q] = (uint32_t)(min(r, t.re - 1 - t.rb) * p.as + du[q] * 8);
     }
+    // (columns past K: zeros at every stage)
     const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ ((wave & 1) << 2);
     const bool cin = kb0 + cunit < KB;
-    const uint8_t* csrc = p.w + (int64_t)t.g * p.N * (p.K / 2) + (kb0 + cunit) * 16;
+    const uint8_t* cbase = p.w + (int64_t)t.g * p.N * (p.K / 2) + kb0 * 16;
+    const uint32_t coff = crow * (uint32_t)(p.K / 2) + cunit * 16;
     const int srow = tid >> 3, sblk = tid & 7;
     const bool sin = kb0 + sblk < KB;
-    const uint8_t* ssrc = p.w_s + (int64_t)t.g * p.N * KB + kb0 + sblk;
+    const uint8_t* sbase = p.w_s + (int64_t)t.g * p.N * KB + kb0;
+    const uint32_t soff = srow * (uint32_t)KB + sblk;
 
     auto issue = [&](int s, int slot) {
-        uint8_t* base = smem + slot * kGSlot;
-        if (VECTOR) {
+        uint8_t* base = smem + slot * kGSlot + wave * 4096;
+        const uint16_t* db = scalar(dbase + s * 64);
+        const uint8_t* cs = scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff;
+        uint8_t* cd = smem + slot * kGSlot + kGDout + wave * 1024;
+        if (s * 64 + 64 <= p.N) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const bool in = s * 64 + du[q] * 8 < p.N;
-                to_lds16(within(in, dsrc[q] + s * 64), base + (wave * 4 + q) * 1024);
+                if (VECTOR) to_lds16(db + doff[q], base + q * 1024);
+                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], 8);
             }
+            to_lds16(within(cin, cs), cd);
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<u32x4_t*>(base + (wave * 4 + q) * 1024 + lane * 16) =
-                    load8_bf16<false>(dsrc[q] + s * 64, p.N - s * 64 - du[q] * 8);
+            for (int q = 0; q < 4; ++q) {
+                const int left = p.N - s * 64 - du[q] * 8;
+                if (VECTOR) to_lds16(within(left > 0, db + doff[q]), base + q * 1024);
+                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], left);
+            }
+            to_lds16(within(cin && s * 64 + crow < p.N, cs), cd);
         }
-        const int n = s * 64 + crow;
-        to_lds16(within(cin && n < p.N, csrc + (int64_t)n * (p.K / 2)), base + kGDout + wave * 1024);
     };
     // scales: byte tid of a stage (row tid / 8, block tid % 8) to a dword of its own
     auto issue_scales = [&](int s, int slot) {
-        const int n = s * 64 + srow;
-        __builtin_amdgcn_global_load_lds(within(sin && n < p.N, ssrc + (int64_t)n * KB),
-                                         (lds_void_t*)(smem + kGOffRaw + slot * kGRaw + wave * 256), 1, 0, 0);
+        to_lds1(within(sin && s * 64 + srow < p.N, scalar(sbase + (int64_t)s * 64 * KB) + soff),
+                smem + kGOffRaw + slot * kGRaw + wave * 256);
     };
-    // and from there, a stage later, to where the operands are decoded
+    // and from there to where the operands are decoded
     auto put_scales = [&](int slot) {
         const uint32_t b = smem[kGOffRaw + slot * kGRaw + tid * 4];
         const uint32_t at = lds_offset(smem) + slot * kGSlot + kGDout + kGCodes + sblk * kGPitch + srow * 2;
@@ -577,62 +665,89 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const int nvi = max(0, min(2, (t.re - t.rb - wt * 64 + 31) >> 5));
     const bool cols = kb0 * 32 + wk * 128 < p.K;
 
-    // Stage s in slot s % 3, issued two ahead, its scales three ahead: they have landed
-    // one step before the others and are rearranged then.  Lane half h of substep q
-    // (16 n) takes rows 16 q + 8 h .. + 8 of the stage.
+    // Stage s in slot s % 3.  Lane half h of substep q (16 n) takes rows 16 q + 8 h .. + 8.
+    // Operands are read one substep ahead, a stage's first ones before the last MFMAs of
+    // the stage before; the barrier stands there, after which the stage's slot is free for
+    // stage s + 3 and the wait has left only the last step's loads in flight.  A stage's
+    // scales are loaded one step earlier than its rest and rearranged in the step before
+    // its own, ahead of that step's barrier.
     auto nloop = [&](auto nv_c) {
         constexpr int NV = decltype(nv_c)::value;
+        uint32_t code[2][8];
+        u32x4_t sc[2], dv[2][2];                          // by parity of the substep
         int slot = 0;
+        auto operands = [&](int sl, int q, auto f_c) {
+            constexpr int f = decltype(f_c)::value;
+            const uint8_t* D = smem + sl * kGSlot;
+            const uint8_t* C = D + kGDout + ((wk ^ h) * 64) + 2 * r32 + (16 * q + 8 * h) * 128;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                dv[f][i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 64 + i * 32 + r32, 2 * q + h));
+            sc[f] = *reinterpret_cast<const u32x4_t*>(D + kGDout + kGCodes + (wk * 4 + (r32 >> 3)) * kGPitch +
+                                                      (16 * q + 8 * h) * 2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) code[f][j] = *reinterpret_cast<const uint16_t*>(C + j * 128);
+        };
+        auto mfmas = [&](auto f_c) {
+            constexpr int f = decltype(f_c)::value;
+            u32x4_t op[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float s0 = __uint_as_float(sc[f][j / 2] << 16), s1 = __uint_as_float(sc[f][j / 2] & 0xFFFF0000u);
+                const uint32_t c0 = code[f][j], c1 = code[f][j + 1];
+                const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 0));
+                const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 1));
+                const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 0));
+                const uint32_t b1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 1));
+                op[0][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+                op[1][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+                op[2][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+                op[3][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
+        };
+        const std::integral_constant<int, 0> c0;
+        const std::integral_constant<int, 1> c1;
+        if constexpr (NV > 0) operands(0, 0, c0);
         for (int s = 0; s < nn; ++s) {
-            const int next = slot == 2 ? 0 : slot + 1, ahead = slot == 0 ? 2 : slot - 1;
-            issue(min(s + 2, nn - 1), ahead);
-            issue_scales(min(s + 3, nn - 1), slot);
+            const int next = slot == 2 ? 0 : slot + 1;
             put_scales(next);
             if constexpr (NV > 0) {
-                const uint8_t* D = smem + slot * kGSlot;
-                const uint8_t* C = D + kGDout + ((wk ^ h) * 64) + 2 * r32;
-                const uint8_t* S = D + kGDout + kGCodes + (wk * 4 + (r32 >> 3)) * kGPitch;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    u32x4_t dv[2];
-#pragma unroll
-                    for (int i = 0; i < NV; ++i)
-                        dv[i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 64 + i * 32 + r32, 2 * q + h));
-                    const u32x4_t sc = *reinterpret_cast<const u32x4_t*>(S + (16 * q + 8 * h) * 2);
-                    u32x4_t op[4];
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const uint32_t c0 = *reinterpret_cast<const uint16_t*>(C + (16 * q + 8 * h + j) * 128);
-                        const uint32_t c1 = *reinterpret_cast<const uint16_t*>(C + (16 * q + 8 * h + j + 1) * 128);
-                        const float s0 = __uint_as_float(sc[j / 2] << 16), s1 = __uint_as_float(sc[j / 2] & 0xFFFF0000u);
-                        const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 0));
-                        const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 1));
-                        const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 0));
-                        const uint32_t b1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 1));
-                        op[0][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
-                        op[1][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
-                        op[2][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
-                        op[3][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[i], acc[c][i]);
-                }
+                operands(slot, 1, c1);
+                keep_order();
+                mfmas(c0);
+                operands(slot, 2, c0);
+                keep_order();
+                mfmas(c1);
+                operands(slot, 3, c1);
+                keep_order();
+                mfmas(c0);
             }
+            keep_order();
             if (VECTOR) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue(min(s + 3, nn - 1), slot);
+            issue_scales(min(s + 4, nn - 1), next);
+            if constexpr (NV > 0) {
+                operands(next, 0, c0);
+                keep_order();
+                mfmas(c1);
+            }
             slot = next;
         }
     };
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
-        if (s < 2) issue(min(s, nn - 1), s);
+        issue(min(s, nn - 1), s);
         issue_scales(min(s, nn - 1), s);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     put_scales(0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    issue_scales(min(3, nn - 1), 0);
     switch (cols ? nvi : 0) {
         case 2: nloop(std::integral_constant<int, 2>{}); break;
         case 1: nloop(std::integral_constant<int, 1>{}); break;
@@ -667,10 +782,10 @@ hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s) {
     const bool aligned =
         p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
     if (p.a_s)
-        return aligned ? launch_tiles<mx_tile_kernel<true>, kMxLds>(p, p.N, s)
-                       : launch_tiles<mx_tile_kernel<false>, kMxLds>(p, p.N, s);
-    return aligned ? launch_tiles<a16_tile_kernel<true>, kALds>(p, p.N, s)
-                   : launch_tiles<a16_tile_kernel<false>, kALds>(p, p.N, s);
+        return aligned ? launch_tiles<mx_tile_kernel<true>, mx_lds(true)>(p, p.N, s)
+                       : launch_tiles<mx_tile_kernel<false>, mx_lds(false)>(p, p.N, s);
+    return aligned ? launch_tiles<a16_tile_kernel<true>, a16_lds(true)>(p, p.N, s)
+                   : launch_tiles<a16_tile_kernel<false>, a16_lds(false)>(p, p.N, s);
 }
 
 hipError_t launch_product_grad_tiles(const ProductArgs& p, hipStream_t s) {
