@@ -232,31 +232,20 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     const uint32_t soff = (wave < 4 ? wrow(srow) : arow(srow)) * (uint32_t)KB;
     const int sdst = 2 * kMxCodes + (wave < 4 ? 0 : kMxScales) + (wave & 3) * 256;
 
-    auto issue = [&](int c, int slot) {
-        uint8_t* base = smem + slot * kMxSlot + wave * 2048;
-        const uint8_t *wb = scalar(wbase + (int64_t)c * 64), *ab = scalar(abase + (int64_t)c * 64);
-        if (ALIGNED || c * 4 + 4 <= KB) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                to_lds16(wb + coff[q], base + q * 1024);
-                to_lds16(ab + aoff[q], base + kMxCodes + q * 1024);
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const bool in = c * 4 + cu[q] < KB;
-                to_lds16(within(in, wb + coff[q]), base + q * 1024);
-                to_lds16(within(in, ab + aoff[q]), base + kMxCodes + q * 1024);
-            }
-        }
-        uint8_t* sd = smem + slot * kMxSlot + sdst;
-        const uint8_t* sb = scalar(sbase + (int64_t)c * 4);
-        if (ALIGNED) {
-            to_lds4(sb + soff, sd);
+    // part 0, 1: the wave's weight codes; 2, 3: the rows' codes; 4: the scales
+    auto issue = [&](int c, int slot, int part) {
+        uint8_t* base = smem + slot * kMxSlot;
+        if (part < 4) {
+            const int q = part & 1;
+            const uint8_t* src = scalar((part < 2 ? wbase : abase) + (int64_t)c * 64) + (part < 2 ? coff[q] : aoff[q]);
+            if (!ALIGNED) src = static_cast<const uint8_t*>(within(c * 4 + cu[q] < KB, src));
+            to_lds16(src, base + (part < 2 ? 0 : kMxCodes) + (wave * 2 + q) * 1024);
+        } else if (ALIGNED) {
+            to_lds4(scalar(sbase + (int64_t)c * 4) + soff, base + sdst);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                to_lds1(within(c * 4 + i < KB, sb + i + soff), sd + i * 1024);
+                to_lds1(within(c * 4 + i < KB, scalar(sbase + (int64_t)c * 4 + i) + soff), base + sdst + i * 1024);
         }
     };
 
@@ -320,17 +309,28 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
             keep_order();
             if (ALIGNED) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            issue(min(c + 4, nc - 1), c & 3);
+            const int ahead = min(c + 4, nc - 1);
             if constexpr (NV > 0) {
                 operands(c + 1, c0);
                 scales(c + 1, g_c);
                 keep_order();
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[j][i] = mfma_mx32<1>(wv[1][j], ws[f][j], av[1][i], as[f][i], acc[j][i]);
             }
+            // the loads one by one between the MFMAs: in a row they would hold up the wave
+            // (and with it the matrix core) until the address unit has taken them all
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (NV > 0) {
+                    if (i < NV) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            acc[j][i] = mfma_mx32<1>(wv[1][j], ws[f][j], av[1][i], as[f][i], acc[j][i]);
+                        keep_order();
+                    }
+                }
+                issue(ahead, c & 3, i);
+                keep_order();
+            }
+            issue(ahead, c & 3, 4);
         };
         if constexpr (NV > 0) {
             operands(0, c0);
@@ -344,7 +344,9 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
         if (c < nc) stage(c, c0, c1);
     };
 #pragma unroll
-    for (int c = 0; c < 4; ++c) issue(min(c, nc - 1), c);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int part = 0; part < 5; ++part) issue(min(c, nc - 1), c, part);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
         case 4: kloop(std::integral_constant<int, 4>{}); break;
@@ -420,37 +422,23 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     }
     const uint32_t soff = wrow((wave & 3) * 64 + lane) * (uint32_t)KB;
 
-    auto issue_rows = [&](int ks, int slot) {
-        uint8_t* base = smem + slot * kARows + wave * 4096;
-        const uint16_t* ab = scalar(abase + (int64_t)ks * 64);
-        if (ALIGNED || ks * 2 + 2 <= KB) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) to_lds16(ab + aoff[q], base + q * 1024);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) to_lds16(within(ks * 8 + au[q] < KB * 4, ab + aoff[q]), base + q * 1024);
-        }
+    auto issue_rows = [&](int ks, int slot, int q) {
+        const uint16_t* src = scalar(abase + (int64_t)ks * 64) + aoff[q];
+        to_lds16(ALIGNED ? src : within(ks * 8 + au[q] < KB * 4, src), smem + slot * kARows + (wave * 4 + q) * 1024);
     };
-    auto issue_weight = [&](int c, int slot) {
+    // part 0, 1: the wave's codes; 2 (and 3 when not ALIGNED): its scales
+    constexpr int kParts = ALIGNED ? 3 : 4;
+    auto issue_weight = [&](int c, int slot, int part) {
         uint8_t* base = smem + kAOffW + slot * kAChunk;
-        const uint8_t *wb = scalar(wbase + (int64_t)c * 64), *sb = scalar(sbase + (int64_t)c * 4);
-        if (ALIGNED || c * 4 + 4 <= KB) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) to_lds16(wb + coff[q], base + (wave * 2 + q) * 1024);
+        if (part < 2) {
+            const uint8_t* src = scalar(wbase + (int64_t)c * 64) + coff[part];
+            to_lds16(ALIGNED ? src : within(c * 4 + cu[part] < KB, src), base + (wave * 2 + part) * 1024);
+        } else if (ALIGNED) {
+            to_lds4(scalar(sbase + (int64_t)c * 4) + soff, base + kMxCodes + (wave & 3) * 256);
         } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                to_lds16(within(c * 4 + cu[q] < KB, wb + coff[q]), base + (wave * 2 + q) * 1024);
-        }
-        if (ALIGNED) {
-            to_lds4(sb + soff, base + kMxCodes + (wave & 3) * 256);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int b = (wave >> 2) * 2 + i;
-                to_lds1(within(c * 4 + b < KB, sb + b + soff),
-                        base + kMxCodes + b * 1024 + (wave & 3) * 256);
-            }
+            const int b = (wave >> 2) * 2 + part - 2;
+            to_lds1(within(c * 4 + b < KB, scalar(sbase + (int64_t)c * 4 + b) + soff),
+                    base + kMxCodes + b * 1024 + (wave & 3) * 256);
         }
     };
 
@@ -495,16 +483,23 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
                 sc[ST][j] = __uint_as_float(sb << 23);
             }
         };
-        auto mfmas = [&](auto st_c, int kk, auto f_c) {
-            constexpr int ST = decltype(st_c)::value, f = decltype(f_c)::value;
-            u32x4_t wv[2];
+        auto mfmas = [&](auto st_c, int kk, auto f_c, auto between) {
+            if constexpr (NV > 0) {
+                constexpr int ST = decltype(st_c)::value, f = decltype(f_c)::value;
+                u32x4_t wv[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[ST][j][kk], sc[ST][j]);
+                for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[ST][j][kk], sc[ST][j]);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[f][i], acc[j][i]);
+                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[f][i], acc[j][i]);
+                    between(i);
+                }
+            }
+#pragma unroll
+            for (int i = NV; i < 4; ++i) between(i);
         };
+        auto nothing = [](int) {};
         const std::integral_constant<int, 0> c0;
         const std::integral_constant<int, 1> c1;
         auto step = [&](int ks, auto st_c, auto next_c) {
@@ -513,25 +508,34 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
             if constexpr (NV > 0) {
                 rows(as, 1, c1);
                 keep_order();
-                mfmas(st_c, 0, c0);
+                mfmas(st_c, 0, c0, nothing);
                 rows(as, 2, c0);
                 keep_order();
-                mfmas(st_c, 1, c1);
+                mfmas(st_c, 1, c1, nothing);
                 rows(as, 3, c1);
                 keep_order();
-                mfmas(st_c, 2, c0);
+                mfmas(st_c, 2, c0, nothing);
             }
             keep_order();
-            if (ALIGNED) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            // only the step before issued anything after the next step's rows: four loads, an
+            // odd one the chunk's too
+            if (ST == 1) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else if (ALIGNED) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            issue_rows(min(ks + 3, nk - 1), as);
-            if (ST == 1) issue_weight(min(ks / 2 + 3, nc - 1), ws);
             if constexpr (NV > 0) {
                 codes(ST == 1 ? wnx : ws, next_c);
                 rows(an, 0, c0);
                 keep_order();
-                mfmas(st_c, 3, c1);
             }
+            // the loads one by one between the MFMAs: in a row they would hold up the wave
+            // (and with it the matrix core) until the address unit has taken them all
+            const int ra = min(ks + 3, nk - 1), ca = min(ks / 2 + 3, nc - 1);
+            mfmas(st_c, 3, c1, [&](int i) {
+                keep_order();
+                issue_rows(ra, as, i);
+                if (ST == 1 && i < kParts) issue_weight(ca, ws, i);
+                keep_order();
+            });
             as = an;
             if (ST == 1) ws = wnx;
         };
@@ -546,8 +550,10 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     };
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        issue_rows(min(i, nk - 1), i);
-        issue_weight(min(i, nc - 1), i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) issue_rows(min(i, nk - 1), i, q);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) issue_weight(min(i, nc - 1), i, q);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
@@ -619,26 +625,18 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const uint8_t* sbase = p.w_s + (int64_t)t.g * p.N * KB + kb0;
     const uint32_t soff = srow * (uint32_t)KB + sblk;
 
-    auto issue = [&](int s, int slot) {
-        uint8_t* base = smem + slot * kGSlot + wave * 4096;
-        const uint16_t* db = scalar(dbase + s * 64);
-        const uint8_t* cs = scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff;
-        uint8_t* cd = smem + slot * kGSlot + kGDout + wave * 1024;
-        if (s * 64 + 64 <= p.N) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (VECTOR) to_lds16(db + doff[q], base + q * 1024);
-                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], 8);
-            }
-            to_lds16(within(cin, cs), cd);
+    // part 0 .. 3: the wave's gradient rows; 4: its weight rows' codes
+    auto issue = [&](int s, int slot, int part) {
+        uint8_t* base = smem + slot * kGSlot;
+        if (part < 4) {
+            const uint16_t* src = scalar(dbase + s * 64) + doff[part];
+            uint8_t* dst = base + (wave * 4 + part) * 1024;
+            const int left = p.N - s * 64 - du[part] * 8;
+            if (VECTOR) to_lds16(within(left > 0, src), dst);
+            else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16<false>(src, left);
         } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int left = p.N - s * 64 - du[q] * 8;
-                if (VECTOR) to_lds16(within(left > 0, db + doff[q]), base + q * 1024);
-                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], left);
-            }
-            to_lds16(within(cin && s * 64 + crow < p.N, cs), cd);
+            to_lds16(within(cin && s * 64 + crow < p.N, scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff),
+                     base + kGDout + wave * 1024);
         }
     };
     // scales: byte tid of a stage (row tid / 8, block tid % 8) to a dword of its own
@@ -688,7 +686,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) code[f][j] = *reinterpret_cast<const uint16_t*>(C + j * 128);
         };
-        auto mfmas = [&](auto f_c) {
+        auto mfmas = [&](auto f_c, auto between) {
             constexpr int f = decltype(f_c)::value;
             u32x4_t op[4];
 #pragma unroll
@@ -707,8 +705,12 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
+                for (int i = 0; i < NV; ++i) {
+                    acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
+                    if (i == NV - 1) between(c);
+                }
         };
+        auto nothing = [](int) {};
         const std::integral_constant<int, 0> c0;
         const std::integral_constant<int, 1> c1;
         if constexpr (NV > 0) operands(0, 0, c0);
@@ -718,30 +720,43 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
             if constexpr (NV > 0) {
                 operands(slot, 1, c1);
                 keep_order();
-                mfmas(c0);
+                mfmas(c0, nothing);
                 operands(slot, 2, c0);
                 keep_order();
-                mfmas(c1);
+                mfmas(c1, nothing);
                 operands(slot, 3, c1);
                 keep_order();
-                mfmas(c0);
+                mfmas(c0, nothing);
             }
             keep_order();
             if (VECTOR) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            issue(min(s + 3, nn - 1), slot);
-            issue_scales(min(s + 4, nn - 1), next);
+            // the loads one by one between the MFMAs (in a row they would hold up the wave
+            // until the address unit has taken them all)
+            auto ahead = [&](int i) {
+                keep_order();
+                issue(min(s + 3, nn - 1), slot, i);
+                if (i == 3) {
+                    issue(min(s + 3, nn - 1), slot, 4);
+                    issue_scales(min(s + 4, nn - 1), next);
+                }
+                keep_order();
+            };
             if constexpr (NV > 0) {
                 operands(next, 0, c0);
                 keep_order();
-                mfmas(c1);
+                mfmas(c1, ahead);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ahead(i);
             }
             slot = next;
         }
     };
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
-        issue(min(s, nn - 1), s);
+#pragma unroll
+        for (int part = 0; part < 5; ++part) issue(min(s, nn - 1), s, part);
         issue_scales(min(s, nn - 1), s);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
