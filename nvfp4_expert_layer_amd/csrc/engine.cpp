@@ -69,10 +69,27 @@ int current_arch_ok(int* dev_out) {
     if (cache[dev] != 1) return fail(MOE_NVFP4_ERR_ARCH, "device %d is not gfx950", dev);
     return MOE_NVFP4_OK;
 }
+
+// Compute units of the current device `dev` (cached per device).
+int cu_count(int dev, int* out) {
+    static std::mutex mu;
+    static int cache[64];
+    std::lock_guard<std::mutex> lk(mu);
+    if (cache[dev] == 0) {
+        int n = 0;
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+            return fail(MOE_NVFP4_ERR_HIP, "hipDeviceGetAttribute(multiprocessor count) failed");
+        cache[dev] = n;
+    }
+    *out = cache[dev];
+    return MOE_NVFP4_OK;
+}
+
 }  // namespace moe
 
 namespace {
 
+using moe::cu_count;
 using moe::current_arch_ok;
 using moe::fail;
 using moe::hip_status;
@@ -194,21 +211,6 @@ void make_plan(const moe_nvfp4_problem& p, Plan& pl) {
     pl.act = take(pl.rows * F * 2);
     pl.Y = take(pl.rows * d * 2);
     pl.total = o;
-}
-
-// Compute units of the current device `dev` (cached per device).
-int cu_count(int dev, int* out) {
-    static std::mutex mu;
-    static int cache[64];
-    std::lock_guard<std::mutex> lk(mu);
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-            return fail(MOE_NVFP4_ERR_HIP, "hipDeviceGetAttribute(multiprocessor count) failed");
-        cache[dev] = n;
-    }
-    *out = cache[dev];
-    return MOE_NVFP4_OK;
 }
 
 int check_weights(const moe_nvfp4_weights* w, const char* what) {

@@ -10,6 +10,7 @@
 
 namespace {
 
+using moe::cu_count;
 using moe::current_arch_ok;
 using moe::fail;
 using moe::hip_status;
@@ -331,12 +332,13 @@ int moe_mxfp4_product(const moe_product_problem* p, const void* a, const uint8_t
                        {"w_scales", w_scales, wn * K / 32, false},
                        {"offsets", offsets, ((size_t)p->groups + 1) * 4, false}};
     if ((st = check_overlap(r))) return st;
-    int dev;
+    int dev, cus;
     if ((st = current_arch_ok(&dev))) return st;
     if (M == 0) return ok();
+    if ((st = cu_count(dev, &cus))) return st;
     moe::ProductArgs g = product_args(p, a, a_stride, w, w_scales, offsets, out, out_dtype, out_stride);
     g.a_s = a_scales;
-    st = hip_status(moe::launch_product(g, static_cast<hipStream_t>(stream)), "MXFP4 product launch");
+    st = hip_status(moe::launch_product(g, cus, static_cast<hipStream_t>(stream)), "MXFP4 product launch");
     return st ? st : ok();
 }
 
@@ -357,11 +359,12 @@ int moe_mxfp4_product_backward(const moe_product_problem* p, const void* dout, i
                        {"w_scales", w_scales, wn * K / 32, false},
                        {"offsets", offsets, ((size_t)p->groups + 1) * 4, false}};
     if ((st = check_overlap(r))) return st;
-    int dev;
+    int dev, cus;
     if ((st = current_arch_ok(&dev))) return st;
     if (M == 0) return ok();
+    if ((st = cu_count(dev, &cus))) return st;
     const moe::ProductArgs g = product_args(p, dout, dout_stride, w, w_scales, offsets, drows, drows_dtype, drows_stride);
-    st = hip_status(moe::launch_product_grad(g, static_cast<hipStream_t>(stream)), "MXFP4 product gradient launch");
+    st = hip_status(moe::launch_product_grad(g, cus, static_cast<hipStream_t>(stream)), "MXFP4 product gradient launch");
     return st ? st : ok();
 }
 

@@ -70,9 +70,10 @@ struct ProductArgs {
     int64_t os;
     int out_vec;                  // rows of out start at multiples of four elements' size
 };
-hipError_t launch_product(const ProductArgs& p, hipStream_t s);
-hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s);  // many rows a group
-hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s);   // a: dout bf16 [M][N]
-hipError_t launch_product_grad_tiles(const ProductArgs& p, hipStream_t s);
+// cus: compute units of the device; a: the rows, or (backward) dout bf16 [M][N]
+hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s);
+hipError_t launch_product_tiles(const ProductArgs& p, int cus, hipStream_t s);  // many rows a group
+hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s);
+hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t s);
 
 }  // namespace moe

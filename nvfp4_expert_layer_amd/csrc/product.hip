@@ -239,13 +239,13 @@ constexpr int kStreamRowsMx = 32, kStreamRowsBf16 = 32, kStreamRowsGrad = 32;
 // The tiles address 256 rows by 32-bit offsets.
 static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 23); }
 
-hipError_t launch_product(const ProductArgs& p, hipStream_t s) {
+hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
     const int64_t few = (int64_t)p.G * (p.a_s ? kStreamRowsMx : kStreamRowsBf16);
-    return p.M <= few || !tiles_reach(p) ? launch_product_stream(p, s) : launch_product_tiles(p, s);
+    return p.M <= few || !tiles_reach(p) ? launch_product_stream(p, s) : launch_product_tiles(p, cus, s);
 }
-hipError_t launch_product_grad(const ProductArgs& p, hipStream_t s) {
+hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
     const int64_t few = (int64_t)p.G * kStreamRowsGrad;
-    return p.M <= few || !tiles_reach(p) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, s);
+    return p.M <= few || !tiles_reach(p) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, cus, s);
 }
 
 }  // namespace moe

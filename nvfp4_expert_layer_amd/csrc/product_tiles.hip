@@ -182,13 +182,16 @@ __device__ __forceinline__ void store_staged(const ProductArgs& p, const uint8_t
 // ---------------------------------------------------------------------------
 // W4A4
 // ---------------------------------------------------------------------------
-constexpr int kMxStages = 4;
-constexpr int kMxCodes = 256 * 64;                          // an operand's 128 k of a stage
-// its scales: a row's four bytes in one dword, or (rows not aligned to dwords) each in
-// one of its own, [4 blocks][256 rows]
-constexpr int mx_scales(bool aligned) { return aligned ? 256 * 4 : 256 * 16; }
-constexpr int mx_slot(bool aligned) { return 2 * kMxCodes + 2 * mx_scales(aligned); }   // codes: weight | rows; scales
-constexpr int mx_lds(bool aligned) { return kMxStages * mx_slot(aligned); }             // 136 or 160 KB
+// Scales of 256 rows and `blocks` blocks in LDS: a row's bytes together, or (rows that
+// are not aligned to dwords) each byte in a dword of its own, [blocks][256 rows].
+constexpr int scale_bytes(bool aligned, int blocks) { return 256 * blocks * (aligned ? 1 : 4); }
+constexpr int kMxCodes = 256 * 128;                         // an operand's 256 k of a stage
+constexpr int mx_slot(bool aligned) { return 2 * kMxCodes + 2 * scale_bytes(aligned, 8); }   // weight | rows; scales
+constexpr int kWaveStage = 2048;                            // a wave's 32 x 32 outputs on their way out
+constexpr int kTable = (1024 + 1) * 4;
+// LDS: stages [2] | waves' staging [8] | table.  Without aligned scales the stages take
+// all 160 KB: one tile a workgroup, staged and looked up in the stages' place.
+constexpr int mx_lds(bool aligned) { return 2 * mx_slot(aligned) + (aligned ? kTWaves * kWaveStage + kTable : 0); }
 
 template <int OPSEL>
 __device__ __forceinline__ f32x16_t mfma_mx32(const u32x4_t& a, uint32_t as, const u32x4_t& b, uint32_t bs,
@@ -197,185 +200,308 @@ __device__ __forceinline__ f32x16_t mfma_mx32(const u32x4_t& a, uint32_t as, con
                                                            OPSEL, (int)bs);
 }
 
+// table[g] = tiles of the groups before g, g = 0 .. G; returns their total.  512
+// threads; ends with a barrier.
+__device__ __forceinline__ int tile_table(const ProductArgs& p, int* table) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int rb = 0, re = 0;
+        if (2 * tid + i < p.G) group_rows(p, 2 * tid + i, rb, re);
+        n[i] = (re - rb + kTM - 1) / kTM;
+    }
+    const int sum = n[0] + n[1];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(inc, o, 64);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 63) table[wave] = inc;
+    __syncthreads();
+    int at = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kTWaves; ++w) {
+        if (w < wave) at += table[w];
+        total += table[w];
+    }
+    __syncthreads();
+    if (2 * tid <= p.G) table[2 * tid] = at;
+    if (2 * tid + 1 <= p.G) table[2 * tid + 1] = at + n[0];
+    if (tid == 0 && p.G == 1024) table[1024] = total;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(total);
+}
+
+// Tile `logical` (tile-major, NT column blocks a tile) by search in the table.
+__device__ __forceinline__ Tile table_tile(const ProductArgs& p, const int* table, int logical, int NT) {
+    const int tile = logical / NT;
+    int lo = 0, hi = p.G;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__builtin_amdgcn_readfirstlane(table[mid]) <= tile) lo = mid;
+        else hi = mid;
+    }
+    int rb, re;
+    group_rows(p, lo, rb, re);
+    rb += (tile - __builtin_amdgcn_readfirstlane(table[lo])) * kTM;
+    return Tile{lo, __builtin_amdgcn_readfirstlane(rb), __builtin_amdgcn_readfirstlane(min(rb + kTM, re)),
+                logical - tile * NT};
+}
+
+// A wave's 32 tokens x 32 outputs (an accumulator) to memory through 2 KB of LDS of its
+// own, without a barrier: tokens' 64-byte rows, whose 16-byte units trade places by row
+// so that both the 8-byte stores and the 16-byte loads spread over all banks.
+__device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage, const Tile& t, int row0, int col0,
+                                           int width, const f32x16_t& acc, bool vec) {
+    const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
+    const int left = width - t.nt * kTN - col0;
+    if (p.out_dtype == kF32) {
+        if (t.rb + row0 + r32 < t.re) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                store4(p.out, kF32, (t.rb + row0 + r32) * p.os + t.nt * kTN + col0 + 8 * g + 4 * h,
+                       f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}, left - 8 * g - 4 * h,
+                       p.out_vec);
+        }
+        return;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        u32x2_t v;
+        if (p.out_dtype == kBF16)
+            v = u32x2_t{f32x2_to_bf16x2(acc[4 * g], acc[4 * g + 1]), f32x2_to_bf16x2(acc[4 * g + 2], acc[4 * g + 3])};
+        else
+            v = u32x2_t{f32_to_f16_bits(acc[4 * g]) | (f32_to_f16_bits(acc[4 * g + 1]) << 16),
+                        f32_to_f16_bits(acc[4 * g + 2]) | (f32_to_f16_bits(acc[4 * g + 3]) << 16)};
+        const uint32_t at = lds_offset(stage) + r32 * 64 + ((g ^ (r32 >> 2)) & 3) * 16 + h * 8;
+        // written out: before an ordinary LDS store the compiler waits for every direct
+        // load in flight.  LDS serves a wave in order: the loads below come after.
+        asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(v) : "memory");
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int r = x * 16 + (lane >> 2), u = lane & 3;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stage + r * 64 + ((u ^ (r >> 2)) & 3) * 16);
+        if (t.rb + row0 + r >= t.re) continue;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (t.rb + row0 + r) * p.os + t.nt * kTN + col0 + 8 * u;
+        if (vec && 8 * u + 8 <= left) {
+            *reinterpret_cast<u32x4_t*>(o) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (8 * u + i < left) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// A workgroup takes tiles one after another: while a tile's last stages are multiplied
+// the next tile's first ones are loaded, and its outputs leave while those land.
 // ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales).
 template <bool ALIGNED>
 __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
-    constexpr int kMxScales = mx_scales(ALIGNED), kMxSlot = mx_slot(ALIGNED);
+    constexpr int kScales = scale_bytes(ALIGNED, 8), kSlot = mx_slot(ALIGNED);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const Tile t = find_tile(p, (p.N + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
-    if (t.g < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int wm = wave >> 2, wn = wave & 3;             // rows 128 wm .. +128, outputs 64 wn .. +64
-    const int KB = p.K / 32, nc = (KB + 3) / 4, n0 = t.nt * kTN;
-    const int64_t w0 = (int64_t)t.g * p.N + n0;
-    const uint8_t* wbase = p.w + w0 * (p.K / 2);
-    const uint8_t* abase = static_cast<const uint8_t*>(p.a) + (int64_t)t.rb * (p.K / 2);
-    // rows and outputs past the tile's end: any valid row (their results are not stored)
-    auto arow = [&](int r) { return (uint32_t)min(r, t.re - 1 - t.rb); };
-    auto wrow = [&](int r) { return (uint32_t)min(r, p.N - 1 - n0); };
+    const int NT = (p.N + kTN - 1) / kTN, KB = p.K / 32, nc = (KB + 7) / 8, r32 = lane & 31;
+    const bool vec = p.os % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 
-    // loads of a stage: per operand 16 KB of codes, two of 1 KB a wave: load q of wave w
-    // fills rows 16 (2 w + q) .. +16, lane i row i / 4, slot i % 4, which holds unit
-    // (i % 4) ^ f(row) of the stage (swz4); scales: 256 bytes a wave, waves 0-3 the
-    // weight's rows 64 w .. +64, waves 4-7 the rows'
-    uint32_t coff[2], aoff[2];
-    int cu[2];
+    // This workgroup's tiles: workgroup b runs on XCD b % 8, each XCD takes a contiguous
+    // range (it shares the tile's rows and the group's weight in its L2), its workgroups
+    // tiles next to each other.
+    int* table = reinterpret_cast<int*>(smem + (ALIGNED ? 2 * kSlot + kTWaves * kWaveStage : 0));
+    const int all = tile_table(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
+    const int end = min(((int)blockIdx.x & 7) * per + per, all);
+    int mine = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+    if (mine >= end) return;
+    Tile t = table_tile(p, table, mine, NT);
+    if (!ALIGNED) __syncthreads();                       // the table's place is a stage's
+
+    // ---- loads, two stages ahead of the multiplication ----
+    // codes of a stage: per operand 32 KB, four loads of 1 KB a wave: load q of wave w
+    // fills rows 8 (4 w + q) .. +8 (a full 128-byte line each), lane i row i / 8, slot
+    // i % 8, which holds unit (i & 7) ^ (i >> 3) ^ (q & 1) (swz8); scales: waves 0-3 the
+    // weight's rows 64 w .. +64, waves 4-7 the rows'.  Rows and outputs past the tile's
+    // end: any valid row (their results are not stored).
+    const uint8_t *wbase, *abase, *sbase;
+    uint32_t coff[4], aoff[4], soff[2];
+    const int cu = (lane & 7) ^ (lane >> 3), srow = (wave & 3) * 64;
+    const int sdst = 2 * kMxCodes + (wave < 4 ? 0 : kScales);
+    auto load_from = [&](const Tile& n) {
+        const int n0 = n.nt * kTN;
+        const int64_t w0 = (int64_t)n.g * p.N + n0;
+        wbase = p.w + w0 * (p.K / 2);
+        abase = static_cast<const uint8_t*>(p.a) + (int64_t)n.rb * (p.K / 2);
+        sbase = wave < 4 ? p.w_s + w0 * KB : p.a_s + (int64_t)n.rb * KB;
+        const int wmax = p.N - 1 - n0, amax = n.re - 1 - n.rb;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int r = (wave * 2 + q) * 16 + (lane >> 2);
-        cu[q] = (lane & 3) ^ (((r >> 1) ^ (r >> 3)) & 3);
-        coff[q] = wrow(r) * (uint32_t)(p.K / 2) + cu[q] * 16;
-        aoff[q] = arow(r) * (uint32_t)(p.K / 2) + cu[q] * 16;
-    }
-    const int srow = (wave & 3) * 64 + lane;
-    const uint8_t* sbase = wave < 4 ? p.w_s + w0 * KB : p.a_s + (int64_t)t.rb * KB;
-    const uint32_t soff = (wave < 4 ? wrow(srow) : arow(srow)) * (uint32_t)KB;
-    const int sdst = 2 * kMxCodes + (wave < 4 ? 0 : kMxScales) + (wave & 3) * 256;
-
-    // part 0, 1: the wave's weight codes; 2, 3: the rows' codes; 4: the scales
+        for (int q = 0; q < 4; ++q) {
+            const int r = (wave * 4 + q) * 8 + (lane >> 3), u = cu ^ (q & 1);
+            coff[q] = min(r, wmax) * (uint32_t)(p.K / 2) + u * 16;
+            aoff[q] = min(r, amax) * (uint32_t)(p.K / 2) + u * 16;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = srow + (ALIGNED ? q * 32 + (lane >> 1) : lane);
+            soff[q] = min(r, wave < 4 ? wmax : amax) * (uint32_t)KB + (ALIGNED ? (lane & 1) * 4 : 0);
+        }
+    };
+    // part 0 .. 3: the wave's codes of both operands; 4: its scales
     auto issue = [&](int c, int slot, int part) {
-        uint8_t* base = smem + slot * kMxSlot;
+        uint8_t* base = smem + slot * kSlot;
         if (part < 4) {
-            const int q = part & 1;
-            const uint8_t* src = scalar((part < 2 ? wbase : abase) + (int64_t)c * 64) + (part < 2 ? coff[q] : aoff[q]);
-            if (!ALIGNED) src = static_cast<const uint8_t*>(within(c * 4 + cu[q] < KB, src));
-            to_lds16(src, base + (part < 2 ? 0 : kMxCodes) + (wave * 2 + q) * 1024);
+            const uint8_t* ws = scalar(wbase + (int64_t)c * 128) + coff[part];
+            const uint8_t* as = scalar(abase + (int64_t)c * 128) + aoff[part];
+            const bool in = c * 8 + (cu ^ (part & 1)) < KB;
+            to_lds16(within(in, ws), base + (wave * 4 + part) * 1024);
+            to_lds16(within(in, as), base + kMxCodes + (wave * 4 + part) * 1024);
         } else if (ALIGNED) {
-            to_lds4(scalar(sbase + (int64_t)c * 4) + soff, base + sdst);
+            const bool in = c * 8 + (lane & 1) * 4 < KB;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                to_lds4(within(in, scalar(sbase + (int64_t)c * 8) + soff[q]), base + sdst + srow * 8 + q * 256);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to_lds1(within(c * 4 + i < KB, scalar(sbase + (int64_t)c * 4 + i) + soff), base + sdst + i * 1024);
+            for (int i = 0; i < 8; ++i)
+                to_lds1(within(c * 8 + i < KB, scalar(sbase + (int64_t)c * 8 + i) + soff[0]),
+                        base + sdst + i * 1024 + srow * 4);
         }
     };
+    int next = mine, ic = 0;                             // tile and stage of the next loads
+    bool more = true;
+    auto advance = [&]() {
+        if (++ic < nc) return;
+        ic = 0;
+        next += stride;
+        more = ALIGNED && next < end;
+        if (more) load_from(table_tile(p, table, next, NT));
+    };
 
+    // ---- the multiplication ----
     f32x16_t acc[2][4];
+    u32x4_t wv[2][2], av[2][4];                          // operands by parity of the MFMA group
+    uint32_t ws[2], as[4], wsn[2], asn[4];               // four blocks' scales; the next stage's
+    auto operands = [&](int slot, auto m_c) {
+        constexpr int m = decltype(m_c)::value, f = m & 1;
+        const uint8_t* S = smem + slot * kSlot;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
+            wv[f][j] = *reinterpret_cast<const u32x4_t*>(S + swz8(wn * 64 + j * 32 + r32, 4 * h + m));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
+            av[f][i] = *reinterpret_cast<const u32x4_t*>(S + kMxCodes + swz8(wm * 128 + i * 32 + r32, 4 * h + m));
+    };
+    auto row_scales = [&](const uint8_t* S, int r) {     // blocks 4 h .. 4 h + 3 of row r
+        if (ALIGNED) return *reinterpret_cast<const uint32_t*>(S + r * 8 + 4 * h);
+        uint32_t v = 0;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
-    const int nvi = max(0, min(4, (t.re - t.rb - wm * 128 + 31) >> 5));      // 32-row blocks with rows
-    const bool cols = n0 + wn * 64 < p.N;
-    const int r32 = lane & 31;
+        for (int i = 0; i < 4; ++i) v |= *reinterpret_cast<const uint32_t*>(S + (4 * h + i) * 1024 + r * 4) << (8 * i);
+        return v;
+    };
+    auto scales = [&](int slot) {
+        const uint8_t* S = smem + slot * kSlot + 2 * kMxCodes;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) wsn[j] = row_scales(S, wn * 64 + j * 32 + r32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asn[i] = row_scales(S + kScales, wm * 128 + i * 32 + r32);
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ws[j] = wsn[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) as[i] = asn[i];
+    };
+    auto mfmas = [&](auto m_c, int i) {
+        constexpr int m = decltype(m_c)::value, f = m & 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j][i] = mfma_mx32<m>(wv[f][j], ws[j], av[f][i], as[i], acc[j][i]);
+    };
 
-    // Stage c sits in slot c % 4.  Lane half h of its MFMA m (0, 1) takes block 2 h + m of
-    // the stage's four.  A step's second operands are read before its first MFMAs, the
-    // next stage's first ones before its second MFMAs, so that the matrix cores do not
-    // wait for LDS; the barrier stands between the two, where the step's slot has been
-    // read and stage c + 4 may take it.  Past the end valid stages are loaded again, so
-    // that each step issues as many loads and the wait leaves the two newer stages in flight.
-    auto kloop = [&](auto nv_c) {
-        constexpr int NV = decltype(nv_c)::value;
-        u32x4_t wv[2][2], av[2][4];
-        uint32_t ws[2][2], as[2][4];                      // scales by parity of the stage
-        auto operands = [&](int c, auto m_c) {
+    // A tile's stages; the running stage sits in `slot`.  Lane half h of MFMA group m
+    // (0 .. 3) takes block 4 h + m of the stage's eight.  A group's operands are read before
+    // the MFMAs of the group before it, so that the matrix cores do not wait for LDS; the
+    // barrier stands before a stage's last MFMAs, where its slot has been read and the
+    // stage after the next may take it.
+    int slot = 0;
+    auto stages = [&](int nv) {                          // nv: 32-row blocks of this wave with rows
+        auto group = [&](auto m_c) {
             constexpr int m = decltype(m_c)::value;
-            const uint8_t* S = smem + (c & 3) * kMxSlot;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                wv[m][j] = *reinterpret_cast<const u32x4_t*>(S + swz4(wn * 64 + j * 32 + r32, 2 * h + m));
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                av[m][i] = *reinterpret_cast<const u32x4_t*>(S + kMxCodes + swz4(wm * 128 + i * 32 + r32, 2 * h + m));
-        };
-        auto scale_pair = [&](const uint8_t* S, int r) {       // blocks 2 h and 2 h + 1 of row r
-            if (ALIGNED) return (uint32_t)*reinterpret_cast<const uint16_t*>(S + r * 4 + 2 * h);
-            return *reinterpret_cast<const uint32_t*>(S + 2048 * h + r * 4) |
-                   (*reinterpret_cast<const uint32_t*>(S + 2048 * h + 1024 + r * 4) << 8);
-        };
-        auto scales = [&](int c, auto f_c) {
-            constexpr int f = decltype(f_c)::value;
-            const uint8_t* S = smem + (c & 3) * kMxSlot + 2 * kMxCodes;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) ws[f][j] = scale_pair(S, wn * 64 + j * 32 + r32);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) as[f][i] = scale_pair(S + kMxScales, wm * 128 + i * 32 + r32);
-        };
-        const std::integral_constant<int, 0> c0;
-        const std::integral_constant<int, 1> c1;
-        auto stage = [&](int c, auto f_c, auto g_c) {
-            constexpr int f = decltype(f_c)::value;
-            if constexpr (NV > 0) {
-                operands(c, c1);
-                keep_order();
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[j][i] = mfma_mx32<0>(wv[0][j], ws[f][j], av[0][i], as[f][i], acc[j][i]);
-            }
+            operands(slot, std::integral_constant<int, m + 1>{});
             keep_order();
-            if (ALIGNED) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            const int ahead = min(c + 4, nc - 1);
-            if constexpr (NV > 0) {
-                operands(c + 1, c0);
-                scales(c + 1, g_c);
-                keep_order();
-            }
-            // the loads one by one between the MFMAs: in a row they would hold up the wave
-            // (and with it the matrix core) until the address unit has taken them all
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < nv) mfmas(m_c, i);
+            keep_order();
+        };
+        for (int c = 0; c < nc; ++c) {
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            group(std::integral_constant<int, 2>{});
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            operands(slot ^ 1, std::integral_constant<int, 0>{});
+            scales(slot ^ 1);
+            keep_order();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (NV > 0) {
-                    if (i < NV) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            acc[j][i] = mfma_mx32<1>(wv[1][j], ws[f][j], av[1][i], as[f][i], acc[j][i]);
-                        keep_order();
-                    }
-                }
-                issue(ahead, c & 3, i);
+                if (i < nv) mfmas(std::integral_constant<int, 3>{}, i);
+                keep_order();
+                if (more) issue(ic, slot, i);
                 keep_order();
             }
-            issue(ahead, c & 3, 4);
-        };
-        if constexpr (NV > 0) {
-            operands(0, c0);
-            scales(0, c0);
+            if (more) {
+                issue(ic, slot, 4);
+                advance();
+            }
+            take_scales();
+            slot ^= 1;
         }
-        int c = 0;
-        for (; c + 1 < nc; c += 2) {
-            stage(c, c0, c1);
-            stage(c + 1, c1, c0);
-        }
-        if (c < nc) stage(c, c0, c1);
     };
+
+    load_from(t);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c) {
+        if (!more) continue;
 #pragma unroll
-        for (int part = 0; part < 5; ++part) issue(min(c, nc - 1), c, part);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    switch (cols ? nvi : 0) {
-        case 4: kloop(std::integral_constant<int, 4>{}); break;
-        case 3: kloop(std::integral_constant<int, 3>{}); break;
-        case 2: kloop(std::integral_constant<int, 2>{}); break;
-        case 1: kloop(std::integral_constant<int, 1>{}); break;
-        default: kloop(std::integral_constant<int, 0>{}); break;
+        for (int part = 0; part < 5; ++part) issue(ic, c, part);
+        advance();
     }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // all loads landed, all reads done
-    if (cols) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    operands(0, std::integral_constant<int, 0>{});
+    scales(0);
+    take_scales();
+    for (;;) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
+        const bool cols = t.nt * kTN + wn * 64 < p.N;
+        const int nvi = cols ? max(0, min(4, (t.re - t.rb - wm * 128 + 31) >> 5)) : 0;   // 32-row blocks with rows
+        stages(nvi);
+        if (!ALIGNED) __syncthreads();                   // staged in the stages' place
+        uint8_t* stage = smem + (ALIGNED ? 2 * kSlot : 0) + wave * kWaveStage;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= nvi) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; v += 4)
-                    stage4(p, smem, t, wm * 128 + i * 32 + r32, wn * 64 + j * 32 + 2 * v + 4 * h, p.N, acc[j][i][v],
-                           acc[j][i][v + 1], acc[j][i][v + 2], acc[j][i][v + 3]);
+                wave_store(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i], vec);
         }
+        mine += stride;
+        if (!ALIGNED || mine >= end) break;
+        t = table_tile(p, table, mine, NT);
     }
-    store_staged(p, smem, t, p.N);
 }
 
 // ---------------------------------------------------------------------------
 // W4A16
 // ---------------------------------------------------------------------------
 constexpr int kARows = 256 * 128;                        // 64 k of the tile's bf16 rows (32 KB)
-constexpr int a16_chunk(bool aligned) { return kMxCodes + mx_scales(aligned); }   // 128 k of the weight
+constexpr int kAWeight = 256 * 64;                        // 128 k of the weight's codes
+constexpr int a16_chunk(bool aligned) { return kAWeight + scale_bytes(aligned, 4); }
 constexpr int kAOffW = 3 * kARows;                       // LDS: rows [3] | weight [3]
 constexpr int a16_lds(bool aligned) { return kAOffW + 3 * a16_chunk(aligned); }   // 147 or 156 KB
 
@@ -422,23 +548,37 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     }
     const uint32_t soff = wrow((wave & 3) * 64 + lane) * (uint32_t)KB;
 
-    auto issue_rows = [&](int ks, int slot, int q) {
-        const uint16_t* src = scalar(abase + (int64_t)ks * 64) + aoff[q];
-        to_lds16(ALIGNED ? src : within(ks * 8 + au[q] < KB * 4, src), smem + slot * kARows + (wave * 4 + q) * 1024);
-    };
-    // part 0, 1: the wave's codes; 2 (and 3 when not ALIGNED): its scales
-    constexpr int kParts = ALIGNED ? 3 : 4;
-    auto issue_weight = [&](int c, int slot, int part) {
-        uint8_t* base = smem + kAOffW + slot * kAChunk;
-        if (part < 2) {
-            const uint8_t* src = scalar(wbase + (int64_t)c * 64) + coff[part];
-            to_lds16(ALIGNED ? src : within(c * 4 + cu[part] < KB, src), base + (wave * 2 + part) * 1024);
-        } else if (ALIGNED) {
-            to_lds4(scalar(sbase + (int64_t)c * 4) + soff, base + kMxCodes + (wave & 3) * 256);
+    auto issue_rows = [&](int ks, int slot) {
+        uint8_t* base = smem + slot * kARows + wave * 4096;
+        const uint16_t* ab = scalar(abase + (int64_t)ks * 64);
+        if (ALIGNED || ks * 2 + 2 <= KB) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) to_lds16(ab + aoff[q], base + q * 1024);
         } else {
-            const int b = (wave >> 2) * 2 + part - 2;
-            to_lds1(within(c * 4 + b < KB, scalar(sbase + (int64_t)c * 4 + b) + soff),
-                    base + kMxCodes + b * 1024 + (wave & 3) * 256);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) to_lds16(within(ks * 8 + au[q] < KB * 4, ab + aoff[q]), base + q * 1024);
+        }
+    };
+    auto issue_weight = [&](int c, int slot) {
+        uint8_t* base = smem + kAOffW + slot * kAChunk;
+        const uint8_t *wb = scalar(wbase + (int64_t)c * 64), *sb = scalar(sbase + (int64_t)c * 4);
+        if (ALIGNED || c * 4 + 4 <= KB) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) to_lds16(wb + coff[q], base + (wave * 2 + q) * 1024);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                to_lds16(within(c * 4 + cu[q] < KB, wb + coff[q]), base + (wave * 2 + q) * 1024);
+        }
+        if (ALIGNED) {
+            to_lds4(sb + soff, base + kAWeight + (wave & 3) * 256);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int b = (wave >> 2) * 2 + i;
+                to_lds1(within(c * 4 + b < KB, sb + b + soff),
+                        base + kAWeight + b * 1024 + (wave & 3) * 256);
+            }
         }
     };
 
@@ -479,27 +619,20 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
             for (int j = 0; j < 2; ++j) {
                 const int r = wn * 64 + j * 32 + r32, b = 2 * ST + h;
                 wc[ST][j] = *reinterpret_cast<const u32x4_t*>(W + swz4(r, b));
-                const uint32_t sb = W[kMxCodes + (ALIGNED ? r * 4 + b : b * 1024 + r * 4)];
+                const uint32_t sb = W[kAWeight + (ALIGNED ? r * 4 + b : b * 1024 + r * 4)];
                 sc[ST][j] = __uint_as_float(sb << 23);
             }
         };
-        auto mfmas = [&](auto st_c, int kk, auto f_c, auto between) {
-            if constexpr (NV > 0) {
-                constexpr int ST = decltype(st_c)::value, f = decltype(f_c)::value;
-                u32x4_t wv[2];
+        auto mfmas = [&](auto st_c, int kk, auto f_c) {
+            constexpr int ST = decltype(st_c)::value, f = decltype(f_c)::value;
+            u32x4_t wv[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[ST][j][kk], sc[ST][j]);
+            for (int j = 0; j < 2; ++j) wv[j] = mx_decode8(wc[ST][j][kk], sc[ST][j]);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[f][i], acc[j][i]);
-                    between(i);
-                }
-            }
-#pragma unroll
-            for (int i = NV; i < 4; ++i) between(i);
+                for (int j = 0; j < 2; ++j) acc[j][i] = mfma_bf16_32(wv[j], av[f][i], acc[j][i]);
         };
-        auto nothing = [](int) {};
         const std::integral_constant<int, 0> c0;
         const std::integral_constant<int, 1> c1;
         auto step = [&](int ks, auto st_c, auto next_c) {
@@ -508,34 +641,25 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
             if constexpr (NV > 0) {
                 rows(as, 1, c1);
                 keep_order();
-                mfmas(st_c, 0, c0, nothing);
+                mfmas(st_c, 0, c0);
                 rows(as, 2, c0);
                 keep_order();
-                mfmas(st_c, 1, c1, nothing);
+                mfmas(st_c, 1, c1);
                 rows(as, 3, c1);
                 keep_order();
-                mfmas(st_c, 2, c0, nothing);
+                mfmas(st_c, 2, c0);
             }
             keep_order();
-            // only the step before issued anything after the next step's rows: four loads, an
-            // odd one the chunk's too
-            if (ST == 1) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else if (ALIGNED) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (ALIGNED) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue_rows(min(ks + 3, nk - 1), as);
+            if (ST == 1) issue_weight(min(ks / 2 + 3, nc - 1), ws);
             if constexpr (NV > 0) {
                 codes(ST == 1 ? wnx : ws, next_c);
                 rows(an, 0, c0);
                 keep_order();
+                mfmas(st_c, 3, c1);
             }
-            // the loads one by one between the MFMAs: in a row they would hold up the wave
-            // (and with it the matrix core) until the address unit has taken them all
-            const int ra = min(ks + 3, nk - 1), ca = min(ks / 2 + 3, nc - 1);
-            mfmas(st_c, 3, c1, [&](int i) {
-                keep_order();
-                issue_rows(ra, as, i);
-                if (ST == 1 && i < kParts) issue_weight(ca, ws, i);
-                keep_order();
-            });
             as = an;
             if (ST == 1) ws = wnx;
         };
@@ -550,10 +674,8 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     };
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) issue_rows(min(i, nk - 1), i, q);
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) issue_weight(min(i, nc - 1), i, q);
+        issue_rows(min(i, nk - 1), i);
+        issue_weight(min(i, nc - 1), i);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
@@ -625,18 +747,26 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const uint8_t* sbase = p.w_s + (int64_t)t.g * p.N * KB + kb0;
     const uint32_t soff = srow * (uint32_t)KB + sblk;
 
-    // part 0 .. 3: the wave's gradient rows; 4: its weight rows' codes
-    auto issue = [&](int s, int slot, int part) {
-        uint8_t* base = smem + slot * kGSlot;
-        if (part < 4) {
-            const uint16_t* src = scalar(dbase + s * 64) + doff[part];
-            uint8_t* dst = base + (wave * 4 + part) * 1024;
-            const int left = p.N - s * 64 - du[part] * 8;
-            if (VECTOR) to_lds16(within(left > 0, src), dst);
-            else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16<false>(src, left);
+    auto issue = [&](int s, int slot) {
+        uint8_t* base = smem + slot * kGSlot + wave * 4096;
+        const uint16_t* db = scalar(dbase + s * 64);
+        const uint8_t* cs = scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff;
+        uint8_t* cd = smem + slot * kGSlot + kGDout + wave * 1024;
+        if (s * 64 + 64 <= p.N) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (VECTOR) to_lds16(db + doff[q], base + q * 1024);
+                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], 8);
+            }
+            to_lds16(within(cin, cs), cd);
         } else {
-            to_lds16(within(cin && s * 64 + crow < p.N, scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff),
-                     base + kGDout + wave * 1024);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int left = p.N - s * 64 - du[q] * 8;
+                if (VECTOR) to_lds16(within(left > 0, db + doff[q]), base + q * 1024);
+                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], left);
+            }
+            to_lds16(within(cin && s * 64 + crow < p.N, cs), cd);
         }
     };
     // scales: byte tid of a stage (row tid / 8, block tid % 8) to a dword of its own
@@ -686,7 +816,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) code[f][j] = *reinterpret_cast<const uint16_t*>(C + j * 128);
         };
-        auto mfmas = [&](auto f_c, auto between) {
+        auto mfmas = [&](auto f_c) {
             constexpr int f = decltype(f_c)::value;
             u32x4_t op[4];
 #pragma unroll
@@ -705,12 +835,8 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
-                    if (i == NV - 1) between(c);
-                }
+                for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
         };
-        auto nothing = [](int) {};
         const std::integral_constant<int, 0> c0;
         const std::integral_constant<int, 1> c1;
         if constexpr (NV > 0) operands(0, 0, c0);
@@ -720,43 +846,30 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
             if constexpr (NV > 0) {
                 operands(slot, 1, c1);
                 keep_order();
-                mfmas(c0, nothing);
+                mfmas(c0);
                 operands(slot, 2, c0);
                 keep_order();
-                mfmas(c1, nothing);
+                mfmas(c1);
                 operands(slot, 3, c1);
                 keep_order();
-                mfmas(c0, nothing);
+                mfmas(c0);
             }
             keep_order();
             if (VECTOR) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            // the loads one by one between the MFMAs (in a row they would hold up the wave
-            // until the address unit has taken them all)
-            auto ahead = [&](int i) {
-                keep_order();
-                issue(min(s + 3, nn - 1), slot, i);
-                if (i == 3) {
-                    issue(min(s + 3, nn - 1), slot, 4);
-                    issue_scales(min(s + 4, nn - 1), next);
-                }
-                keep_order();
-            };
+            issue(min(s + 3, nn - 1), slot);
+            issue_scales(min(s + 4, nn - 1), next);
             if constexpr (NV > 0) {
                 operands(next, 0, c0);
                 keep_order();
-                mfmas(c1, ahead);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ahead(i);
+                mfmas(c1);
             }
             slot = next;
         }
     };
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
-#pragma unroll
-        for (int part = 0; part < 5; ++part) issue(min(s, nn - 1), s, part);
+        issue(min(s, nn - 1), s);
         issue_scales(min(s, nn - 1), s);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -785,27 +898,30 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 }
 
 template <auto Kern, int LDS>
-static hipError_t launch_tiles(const ProductArgs& p, int width, hipStream_t s) {
+static hipError_t launch_tiles(const ProductArgs& p, int64_t grid, hipStream_t s) {
     const hipError_t e = allow_dynamic_lds<Kern>(LDS);
     if (e != hipSuccess) return e;
-    const int64_t grid = tile_grid(p, (width + kTN - 1) / kTN);
     hipLaunchKernelGGL(Kern, dim3((unsigned)grid), dim3(kTThreads), LDS, s, p);
     return hipGetLastError();
 }
 
-hipError_t launch_product_tiles(const ProductArgs& p, hipStream_t s) {
+hipError_t launch_product_tiles(const ProductArgs& p, int cus, hipStream_t s) {
     const bool aligned =
         p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
+    const int64_t tiles = tile_grid(p, (p.N + kTN - 1) / kTN);
+    // one workgroup a CU, each for several tiles, or (tiles: a multiple of 8) one a tile
+    const int64_t one_each = min(tiles, (int64_t)max(cus / 8 * 8, 8));
     if (p.a_s)
-        return aligned ? launch_tiles<mx_tile_kernel<true>, mx_lds(true)>(p, p.N, s)
-                       : launch_tiles<mx_tile_kernel<false>, mx_lds(false)>(p, p.N, s);
-    return aligned ? launch_tiles<a16_tile_kernel<true>, a16_lds(true)>(p, p.N, s)
-                   : launch_tiles<a16_tile_kernel<false>, a16_lds(false)>(p, p.N, s);
+        return aligned ? launch_tiles<mx_tile_kernel<true>, mx_lds(true)>(p, one_each, s)
+                       : launch_tiles<mx_tile_kernel<false>, mx_lds(false)>(p, tiles, s);
+    return aligned ? launch_tiles<a16_tile_kernel<true>, a16_lds(true)>(p, tiles, s)
+                   : launch_tiles<a16_tile_kernel<false>, a16_lds(false)>(p, tiles, s);
 }
 
-hipError_t launch_product_grad_tiles(const ProductArgs& p, hipStream_t s) {
-    return dout_vector(p) ? launch_tiles<grad_tile_kernel<true>, kGLdsAll>(p, p.K, s)
-                          : launch_tiles<grad_tile_kernel<false>, kGLdsAll>(p, p.K, s);
+hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t s) {
+    const int64_t tiles = tile_grid(p, (p.K + kTN - 1) / kTN);
+    return dout_vector(p) ? launch_tiles<grad_tile_kernel<true>, kGLdsAll>(p, tiles, s)
+                          : launch_tiles<grad_tile_kernel<false>, kGLdsAll>(p, tiles, s);
 }
 
 }  // namespace moe

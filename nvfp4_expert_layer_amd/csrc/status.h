@@ -9,5 +9,6 @@ int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)))
 int ok();                                              // clears the message, returns OK
 int hip_status(hipError_t e, const char* where);       // OK, or MOE_NVFP4_ERR_HIP with a message
 int current_arch_ok(int* dev_out);                     // OK iff the current device is gfx950
+int cu_count(int dev, int* out);                       // compute units of the current device `dev`
 
 }  // namespace moe
