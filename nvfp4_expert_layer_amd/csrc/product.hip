@@ -127,15 +127,179 @@ __global__ __launch_bounds__(64 * kSWaves) void product_stream_kernel(ProductArg
     }
 }
 
-hipError_t launch_product_stream(const ProductArgs& p, hipStream_t s) {
-    const int groups = min(p.G, p.M);                           // at most so many hold rows
-    const dim3 grid((p.N + 15) / 16, groups);
-    const int by_rank = p.M < p.G ? 1 : 0;
-    if (p.a_s)
-        hipLaunchKernelGGL((product_stream_kernel<true, 1>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+// ---------------------------------------------------------------------------
+// forward, K up to 4096 (W4A4: 8192): eight waves split K into contiguous parts of KS steps (128 k),
+// each keeps its part of the tokens in registers and walks the workgroup's weight
+// tiles (16 rows) with the codes of the next two in flight, so that only weights
+// stream; one barrier a tile joins the waves' sums.
+// ---------------------------------------------------------------------------
+constexpr int kRWaves = 8;
+
+template <bool MX, int KS, int NT, bool S16>
+__device__ __forceinline__ void resident_tiles(const ProductArgs& p, int g, int r0, int re, int t0, int t1,
+                                               f32x4_t* red) {
+    constexpr int TQ = MX ? 1 : 4;                              // 16-byte operands of a block's tokens
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, lg = lane >> 4, KB = p.K / 32;
+    const int kb0 = wave * KS * 4 + lg;                         // this lane's block of step s: kb0 + 4 s
+    u32x4_t tok[KS][NT][TQ];
+    uint32_t ts[KS][NT];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 16 * t + col, kb = kb0 + 4 * s;
+            const bool v = r < re && kb < KB;
+            ts[s][t] = 0u;
+            if (MX && v) ts[s][t] = p.a_s[(int64_t)r * KB + kb];
+#pragma unroll
+            for (int q = 0; q < TQ; ++q) {
+                tok[s][t][q] = u32x4_t{0u, 0u, 0u, 0u};
+                if (v)
+                    tok[s][t][q] = MX ? *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p.a) +
+                                                                          (int64_t)r * (p.K / 2) + kb * 16)
+                                      : *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.a) +
+                                                                          r * p.as + kb * 32 + 8 * q);
+            }
+        }
+    struct Weight {
+        u32x4_t c[KS];
+        uint32_t s[KS];
+    };
+    const uint8_t* wbase = p.w + (int64_t)g * p.N * (p.K / 2);
+    const uint8_t* sbase = p.w_s + (int64_t)g * p.N * KB;
+    // blocks past K: any valid block's codes (the tokens there are 0) under scale 2^0, for
+    // 0 times a NaN scale would not be 0
+    auto load = [&](int t, Weight& w) {
+        const int64_t n = min(t * 16 + col, p.N - 1);           // rows past N: any valid row
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            w.c[s] = *reinterpret_cast<const u32x4_t*>(wbase + n * (p.K / 2) + min(kb0 + 4 * s, KB - 1) * 16);
+        if constexpr (S16) {                                    // KS dwords of the row: byte lg of dword s
+            const uint8_t* sr = sbase + n * KB + min(wave * KS * 4, KB - KS * 4);
+            if constexpr (KS >= 4) {
+#pragma unroll
+                for (int s = 0; s < KS; s += 4) {
+                    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(sr + 4 * s);
+                    w.s[s] = v.x; w.s[s + 1] = v.y; w.s[s + 2] = v.z; w.s[s + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < KS; ++s) w.s[s] = *reinterpret_cast<const uint32_t*>(sr + 4 * s);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) w.s[s] = sbase[n * KB + min(kb0 + 4 * s, KB - 1)];
+        }
+    };
+    auto tile = [&](int t, Weight& w) {
+        f32x4_t acc[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            uint32_t sb = S16 ? (w.s[s] >> (8 * lg)) & 0xFFu : w.s[s];
+            if (kb0 + 4 * s >= KB) sb = 127u;
+            if constexpr (MX) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) acc[i] = mfma_mx16(w.c[s], sb, tok[s][i][0], ts[s][i], acc[i]);
+            } else {
+                const float sc = __uint_as_float(sb << 23);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const u32x4_t wv = mx_decode8(w.c[s][q], sc);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) acc[i] = mfma_bf16_16(wv, tok[s][i][q], acc[i]);
+                }
+            }
+        }
+        if (t + 2 < t1) load(t + 2, w);
+        f32x4_t* buf = red + (t & 1) * kRWaves * NT * 64;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) buf[(wave * NT + i) * 64 + lane] = acc[i];
+        // (a plain barrier would wait for the loads in flight.)  Two buffers: the tile after
+        // the next writes this one again only after the next tile's barrier
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if (((t * NT + i) & (kRWaves - 1)) != wave) continue;
+            f32x4_t sum = buf[i * 64 + lane];
+#pragma unroll
+            for (int v = 1; v < kRWaves; ++v) sum += buf[(v * NT + i) * 64 + lane];
+            const int r = r0 + 16 * i + col, n = t * 16 + 4 * lg;
+            if (r < re) store4(p.out, p.out_dtype, r * p.os + n, sum, p.N - n, p.out_vec);
+        }
+    };
+    Weight w0, w1;
+    load(t0, w0);
+    if (t0 + 1 < t1) load(t0 + 1, w1);
+    for (int t = t0; t < t1; t += 2) {
+        tile(t, w0);
+        if (t + 1 < t1) tile(t + 1, w1);
+    }
+    // both buffers are free before the next rows' tiles write them
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <bool MX, int KS, int MAXT, bool S16>
+__global__ __launch_bounds__(64 * kRWaves) void product_resident_kernel(ProductArgs p, int by_rank, int per_block) {
+    __shared__ f32x4_t red[2 * kRWaves * MAXT * 64];
+    const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
+    if (g < 0) return;
+    int rb, re;
+    group_rows(p, g, rb, re);
+    const int t0 = blockIdx.x * per_block, t1 = min(t0 + per_block, (p.N + 15) / 16);
+    for (int r0 = rb; r0 < re;) {
+        if (MAXT > 1 && re - r0 > 16) {
+            resident_tiles<MX, KS, MAXT, S16>(p, g, r0, re, t0, t1, red);
+            r0 += 16 * MAXT;
+        } else {
+            resident_tiles<MX, KS, 1, S16>(p, g, r0, re, t0, t1, red);
+            r0 += 16;
+        }
+    }
+}
+
+template <bool MX, int KS, int MAXT>
+static void launch_resident(const ProductArgs& p, int cus, int groups, int by_rank, hipStream_t s) {
+    // tiles a workgroup: as many as leave four workgroups a CU
+    const int tiles = (p.N + 15) / 16;
+    const int per = max(1, min(16, (int)((int64_t)tiles * groups / (4 * cus))));
+    const dim3 grid((tiles + per - 1) / per, groups);
+    // a wave's part of a scale row is one aligned load (per 16 bytes)
+    constexpr int part = KS >= 4 ? 16 : 4 * KS;
+    const bool s16 = p.K % (128 * KS) == 0 && (p.K / 32) % part == 0 &&
+                     (reinterpret_cast<uintptr_t>(p.w_s) & (part - 1)) == 0;
+    if (s16)
+        hipLaunchKernelGGL((product_resident_kernel<MX, KS, MAXT, true>), grid, dim3(64 * kRWaves), 0, s, p, by_rank,
+                           per);
     else
-        hipLaunchKernelGGL((product_stream_kernel<false, 1>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+        hipLaunchKernelGGL((product_resident_kernel<MX, KS, MAXT, false>), grid, dim3(64 * kRWaves), 0, s, p, by_rank,
+                           per);
+}
+
+template <bool MX>
+static hipError_t launch_stream(const ProductArgs& p, int cus, hipStream_t s) {
+    const int groups = min(p.G, p.M);                           // at most so many hold rows
+    const int by_rank = p.M < p.G ? 1 : 0;
+    // up to 8 rows a group on average: most groups fit 16 tokens, and the registers that
+    // 32 tokens would take keep more weights in flight
+    const bool one = p.M <= 8 * groups;
+#define RESIDENT(KS) \
+    (one ? launch_resident<MX, KS, 1>(p, cus, groups, by_rank, s) : launch_resident<MX, KS, 2>(p, cus, groups, by_rank, s))
+    if (p.K <= 1024) RESIDENT(1);
+    else if (p.K <= 2048) RESIDENT(2);
+    else if (p.K <= 4096) RESIDENT(4);
+    else if (MX && p.K <= 8192) launch_resident<true, 8, 1>(p, cus, groups, by_rank, s);
+    else
+        hipLaunchKernelGGL((product_stream_kernel<MX, 1>), dim3((p.N + 15) / 16, groups), dim3(64 * kSWaves), 0, s, p,
+                           by_rank);
+#undef RESIDENT
     return hipGetLastError();
+}
+
+hipError_t launch_product_stream(const ProductArgs& p, int cus, hipStream_t s) {
+    return p.a_s ? launch_stream<true>(p, cus, s) : launch_stream<false>(p, cus, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -241,7 +405,7 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 23); }
 
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
     const int64_t few = (int64_t)p.G * (p.a_s ? kStreamRowsMx : kStreamRowsBf16);
-    return p.M <= few || !tiles_reach(p) ? launch_product_stream(p, s) : launch_product_tiles(p, cus, s);
+    return p.M <= few || !tiles_reach(p) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
 }
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
     const int64_t few = (int64_t)p.G * kStreamRowsGrad;
