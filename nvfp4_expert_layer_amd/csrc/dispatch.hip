@@ -206,24 +206,21 @@ __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a
     for (int e = tid; e < a.L; e += kThreads) a.block_counts[(size_t)e * blocks + blockIdx.x] = hist[e];
 }
 
-// Second: per expert, an exclusive scan over the blocks (a wave each) and the total.
+// Second: per expert (a workgroup each), an exclusive scan over the blocks and the total.
 __global__ __launch_bounds__(kThreads) void dispatch_scan_kernel(DispatchArgs a, int blocks) {
-    const int e = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (e >= a.L) return;
-    int32_t* c = a.block_counts + (size_t)e * blocks;
+    __shared__ int v[kMaxExperts], part[4];
+    int32_t* c = a.block_counts + (size_t)blockIdx.x * blocks;
     int sum = 0;
-    for (int b0 = 0; b0 < blocks; b0 += 64) {
-        const int b = b0 + lane, x = b < blocks ? c[b] : 0;
-        int inc = x;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int y = __shfl_up(inc, o, 64);
-            if (lane >= o) inc += y;
-        }
-        if (b < blocks) c[b] = sum + inc - x;
-        sum += __shfl(inc, 63, 64);
+    for (int b0 = 0; b0 < blocks; b0 += kMaxExperts) {
+        const int n = min(blocks - b0, kMaxExperts);
+        for (int i = threadIdx.x; i < n; i += kThreads) v[i] = c[b0 + i];
+        __syncthreads();
+        const int total = block_scan(v, n, part);
+        for (int i = threadIdx.x; i < n; i += kThreads) c[b0 + i] = sum + v[i];
+        __syncthreads();
+        sum += total;
     }
-    if (lane == 0) a.totals[e] = sum;
+    if (threadIdx.x == 0) a.totals[blockIdx.x] = sum;
 }
 
 // Up to this many pairs each block counts them all by itself.
@@ -231,13 +228,12 @@ constexpr int kOneLaunchPairs = 16384;
 
 DispatchPlan dispatch_plan(int T, int k) {
     DispatchPlan p;
-    // one token a block until there are blocks enough to fill the card, then as
-    // many as keep a block's pairs within kChunk
-    const int most = kChunk / k;
-    int tpb = T / 1024;
-    p.tokens_per_block = tpb < 1 ? 1 : (tpb > most ? most : tpb);
-    p.blocks = (T + p.tokens_per_block - 1) / p.tokens_per_block;
     p.one_launch = (int64_t)T * k <= kOneLaunchPairs;
+    // one launch: one token a block until there are blocks enough to fill the card; else
+    // whole chunks, for each block leaves a count per expert
+    const int most = kChunk / k, few = T / 1024 < 1 ? 1 : T / 1024;
+    p.tokens_per_block = !p.one_launch || few > most ? most : few;
+    p.blocks = (T + p.tokens_per_block - 1) / p.tokens_per_block;
     return p;
 }
 
@@ -245,14 +241,11 @@ template <typename U>
 static void dispatch_units(const DispatchArgs& a, const DispatchPlan& p, hipStream_t s) {
     const int eb = dtype_bytes(a.dtype), per = (int)sizeof(U) / eb;
     const int units = a.x ? a.d / per : 0;
-    // few tokens: columns over several blocks too
-    int split = 1;
-    if (p.blocks < 256) {
-        const int most = (units + 63) / 64;
-        split = 256 / p.blocks;
-        split = split > most ? most : split;
-        if (split < 1) split = 1;
-    }
+    // few blocks: the columns over several too, at least 64 units each
+    const int want = p.one_launch ? 256 : 2048, most = (units + 63) / 64;
+    int split = want / p.blocks;
+    split = split > most ? most : split;
+    if (split < 1) split = 1;
     const dim3 grid(p.blocks, split);
     if (p.one_launch) {
         hipLaunchKernelGGL((dispatch_kernel<U, false>), grid, dim3(kThreads), 0, s, a, p.tokens_per_block, p.blocks,
@@ -260,7 +253,7 @@ static void dispatch_units(const DispatchArgs& a, const DispatchPlan& p, hipStre
         return;
     }
     hipLaunchKernelGGL(dispatch_count_kernel, dim3(p.blocks), dim3(kThreads), 0, s, a, p.tokens_per_block, p.blocks);
-    hipLaunchKernelGGL(dispatch_scan_kernel, dim3((a.L + 3) / 4), dim3(kThreads), 0, s, a, p.blocks);
+    hipLaunchKernelGGL(dispatch_scan_kernel, dim3(a.L), dim3(kThreads), 0, s, a, p.blocks);
     hipLaunchKernelGGL((dispatch_kernel<U, true>), grid, dim3(kThreads), 0, s, a, p.tokens_per_block, p.blocks, units,
                        a.xs / per, a.rs / per);
 }

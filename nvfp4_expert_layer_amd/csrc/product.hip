@@ -309,72 +309,91 @@ hipError_t launch_product_stream(const ProductArgs& p, int cus, hipStream_t s) {
 // regroups them by column (v_perm); operand c of the eight then holds columns
 // 8 i + c for operand row i, and a lane ends with eight consecutive outputs.
 // ---------------------------------------------------------------------------
+constexpr int kGWaves = 8;
+
 template <int NT, bool VECTOR>
 __device__ __forceinline__ void grad_tiles(const ProductArgs& p, int g, int r0, int re, int k0, float* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
     const int KB = p.K / 32, kc = k0 + 8 * col;                 // this lane's columns kc .. kc + 7
     const bool kv = kc < p.K;                                   // K is a multiple of 32: all eight or none
-    const uint8_t* wbase = p.w + (int64_t)g * p.N * (p.K / 2) + kc / 2;
-    const uint8_t* sbase = p.w_s + (int64_t)g * p.N * KB + kc / 32;
+    const uint8_t* wbase = p.w + (int64_t)g * p.N * (p.K / 2) + (kv ? kc / 2 : 0);
+    const uint8_t* sbase = p.w_s + (int64_t)g * p.N * KB + (kv ? kc / 32 : 0);
     const uint16_t* dout = static_cast<const uint16_t*>(p.a);
     f32x4_t acc[8][NT];
 #pragma unroll
     for (int c = 0; c < 8; ++c)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[c][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int ns = wave * 32; ns < p.N; ns += 32 * kSWaves) {
-        const int n = ns + 8 * lg;                              // this lane's rows n .. n + 7
+    // a step: 32 weight rows, eight a lane group; loaded one step ahead
+    struct Step {
         uint32_t code[8], sb[8];
+        u32x4_t dv[NT];
+    };
+    auto load = [&](int ns, Step& st) {
+        const int n = ns + 8 * lg;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            code[j] = sb[j] = 0u;
-            if (kv && n + j < p.N) {
-                code[j] = *reinterpret_cast<const uint32_t*>(wbase + (int64_t)(n + j) * (p.K / 2));
-                sb[j] = sbase[(int64_t)(n + j) * KB];
-            }
+            // rows past N: the last one, against zeros of dout; its scale is masked below
+            const int64_t row = min(n + j, p.N - 1);
+            st.code[j] = *reinterpret_cast<const uint32_t*>(wbase + row * (p.K / 2));
+            st.sb[j] = sbase[row * KB];
         }
-        u32x4_t dv[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + col;
-            dv[t] = r < re ? load8_bf16<VECTOR>(dout + r * p.as + n, p.N - n) : u32x4_t{0u, 0u, 0u, 0u};
+            st.dv[t] = r < re ? load8_bf16<VECTOR>(dout + r * p.as + n, p.N - n) : u32x4_t{0u, 0u, 0u, 0u};
+        }
+    };
+    auto multiply = [&](int ns, Step& st) {
+        if (ns + 32 > p.N) {                                    // (0 times a NaN scale would not be 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (ns + 8 * lg + j >= p.N) st.sb[j] = 127u;
         }
         u32x4_t op[8];
-        mx_decode_columns(code, sb, op);
+        mx_decode_columns(st.code, st.sb, op);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[c][t] = mfma_bf16_16(op[c], dv[t], acc[c][t]);
+            for (int t = 0; t < NT; ++t) acc[c][t] = mfma_bf16_16(op[c], st.dv[t], acc[c][t]);
+    };
+    constexpr int STRIDE = 32 * kGWaves;
+    Step s0, s1;
+    int ns = wave * 32;
+    if (ns < p.N) load(ns, s0);
+    for (; ns < p.N; ns += 2 * STRIDE) {
+        if (ns + STRIDE < p.N) load(ns + STRIDE, s1);
+        multiply(ns, s0);
+        if (ns + STRIDE >= p.N) break;
+        if (ns + 2 * STRIDE < p.N) load(ns + 2 * STRIDE, s0);
+        multiply(ns + STRIDE, s1);
     }
-    // red [wave][t][v][c][lane]: a lane's eight columns of output row v
-    __syncthreads();                                            // red's previous readers are done
+    // join the waves' sums, 16 tokens at a time: red [wave][v][c][lane]
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+        __syncthreads();                                        // red's previous readers are done
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) red[(((wave * NT + t) * 4 + v) * 8 + c) * 64 + lane] = acc[c][t][v];
-    __syncthreads();
-    for (int x = threadIdx.x; x < NT * 4 * 64; x += 64 * kSWaves) {
-        const int l = x & 63, v = (x >> 6) & 3, t = x >> 8;
-        float f[8];
+            for (int v = 0; v < 4; ++v) red[((wave * 4 + v) * 8 + c) * 64 + lane] = acc[c][t][v];
+        __syncthreads();
+        // thread: lane l, value v, half q of its eight columns
+        const int l = threadIdx.x & 63, v = (threadIdx.x >> 6) & 3, q = threadIdx.x >> 8;
+        f32x4_t f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            f[c] = red[((t * 4 + v) * 8 + c) * 64 + l];
+        for (int c = 0; c < 4; ++c) {
+            f[c] = red[(v * 8 + 4 * q + c) * 64 + l];
 #pragma unroll
-            for (int w = 1; w < kSWaves; ++w) f[c] += red[(((w * NT + t) * 4 + v) * 8 + c) * 64 + l];
+            for (int w = 1; w < kGWaves; ++w) f[c] += red[((w * 4 + v) * 8 + 4 * q + c) * 64 + l];
         }
-        const int r = r0 + 16 * t + (l & 15), k = k0 + 8 * (4 * (l >> 4) + v);
-        if (r < re && k < p.K) {
-            store4(p.out, p.out_dtype, r * p.os + k, f32x4_t{f[0], f[1], f[2], f[3]}, 4, p.out_vec);
-            store4(p.out, p.out_dtype, r * p.os + k + 4, f32x4_t{f[4], f[5], f[6], f[7]}, 4, p.out_vec);
-        }
+        const int r = r0 + 16 * t + (l & 15), k = k0 + 8 * (4 * (l >> 4) + v) + 4 * q;
+        if (r < re && k < p.K) store4(p.out, p.out_dtype, r * p.os + k, f, 4, p.out_vec);
     }
 }
 
 template <bool VECTOR>
-__global__ __launch_bounds__(64 * kSWaves) void product_grad_stream_kernel(ProductArgs p, int by_rank) {
-    __shared__ float red[kSWaves * 2 * 32 * 64];
+__global__ __launch_bounds__(64 * kGWaves) void product_grad_stream_kernel(ProductArgs p, int by_rank) {
+    __shared__ float red[kGWaves * 32 * 64];
     const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
     if (g < 0) return;
     int rb, re;
@@ -391,25 +410,34 @@ hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
     const dim3 grid((p.K + 127) / 128, groups);
     const int by_rank = p.M < p.G ? 1 : 0;
     if (dout_vector(p))
-        hipLaunchKernelGGL((product_grad_stream_kernel<true>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+        hipLaunchKernelGGL((product_grad_stream_kernel<true>), grid, dim3(64 * kGWaves), 0, s, p, by_rank);
     else
-        hipLaunchKernelGGL((product_grad_stream_kernel<false>), grid, dim3(64 * kSWaves), 0, s, p, by_rank);
+        hipLaunchKernelGGL((product_grad_stream_kernel<false>), grid, dim3(64 * kGWaves), 0, s, p, by_rank);
     return hipGetLastError();
 }
-
-// Rows a group (an upper bound of their mean) up to which the weight is streamed.
-constexpr int kStreamRowsMx = 32, kStreamRowsBf16 = 32, kStreamRowsGrad = 32;
 
 // The tiles address 256 rows by 32-bit offsets.
 static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 23); }
 
+// Rows a group (M / G, an upper bound of their mean) up to which the weight is streamed
+// past the tokens instead of multiplied in 256 x 256 tiles.  Measured on 64 groups of
+// 2048 x 4096, us streamed against tiled: W4A16 77 / 110 at 16 rows, 124 / 119 at 32;
+// W4A4 59 / 72 and 96 / 75; backward 127 / 135 and 179 / 164.  Tiles that leave most of
+// the card idle lose for longer (one group of 4096 x 4096: W4A16 38 / 54 at 128 rows,
+// 74 / 85 at 256; W4A4 24 / 27 at 128; backward 63 / 75 at 128; eight groups of 2048 x
+// 4096 cross at about 32 again): the bound grows with the CUs that the tiles of one row
+// block leave four times over.
+static bool streamed(const ProductArgs& p, int rows, int width, int cus) {
+    const int64_t tiles = (int64_t)p.G * ((width + 255) / 256);
+    const int64_t idle = cus / (4 * tiles);
+    return p.M <= p.G * rows * (idle > 1 ? idle : 1) || !tiles_reach(p);
+}
+
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
-    const int64_t few = (int64_t)p.G * (p.a_s ? kStreamRowsMx : kStreamRowsBf16);
-    return p.M <= few || !tiles_reach(p) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
+    return streamed(p, p.a_s ? 20 : 24, p.N, cus) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
 }
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
-    const int64_t few = (int64_t)p.G * kStreamRowsGrad;
-    return p.M <= few || !tiles_reach(p) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, cus, s);
+    return streamed(p, 24, p.K, cus) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, cus, s);
 }
 
 }  // namespace moe
