@@ -60,20 +60,23 @@ struct Row {
         if constexpr (!VECTOR || sizeof(E) == 4) return to_f32<DT>(r.w[i]);
         else return to_f32<DT>((i & 1) ? r.w[i / 2] >> 16 : r.w[i / 2] & 0xFFFFu);
     }
+    // Streaming stores: a row is written once and read by the next kernel at the earliest
+    // (T=8192, d=4096: gradient rows alone 149 -> 104 us, combine 116 -> 109 us).
     static __device__ __forceinline__ void store(void* base, int64_t el, const float (&f)[VEC]) {
         E* p = static_cast<E*>(base) + el;
         if constexpr (!VECTOR) {
             *p = (E)from_f32<DT>(f[0]);
         } else if constexpr (sizeof(E) == 4) {
-            *reinterpret_cast<u32x4_t*>(p) = u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]),
-                                                     __float_as_uint(f[2]), __float_as_uint(f[3])};
+            __builtin_nontemporal_store(u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                                __float_as_uint(f[3])},
+                                        reinterpret_cast<u32x4_t*>(p));
         } else {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 o[i] = DT == kBF16 ? f32x2_to_bf16x2(f[2 * i], f[2 * i + 1])
                                    : from_f32<DT>(f[2 * i]) | (from_f32<DT>(f[2 * i + 1]) << 16);
-            *reinterpret_cast<u32x4_t*>(p) = u32x4_t{o[0], o[1], o[2], o[3]};
+            __builtin_nontemporal_store(u32x4_t{o[0], o[1], o[2], o[3]}, reinterpret_cast<u32x4_t*>(p));
         }
     }
 };
@@ -181,12 +184,24 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a, int 
     U* rows = static_cast<U*>(a.rows);
     const int per = (units + gridDim.y - 1) / gridDim.y, u0 = blockIdx.y * per, nu = min(per, units - u0);
     if (nu <= 0) return;
-    for (int i = tid; i < nt * nu; i += kThreads) {
-        const int t = i / nu, u = u0 + (i - t * nu);
-        const U v = x[(t0 + t) * xs + u];
-        for (int j = 0; j < a.k; ++j) {
-            const int r = dest[t * a.k + j];
-            if (r >= 0) rows[r * rs + u] = v;
+    // four units a thread at a time: their loads first, then each one's k stores
+    for (int i0 = tid; i0 < nt * nu; i0 += 4 * kThreads) {
+        U v[4];
+        int t[4], u[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q * kThreads;
+            t[q] = i / nu;
+            u[q] = u0 + (i - t[q] * nu);
+            if (i < nt * nu) v[q] = x[(t0 + t[q]) * xs + u[q]];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (i0 + q * kThreads >= nt * nu) break;
+            for (int j = 0; j < a.k; ++j) {
+                const int r = dest[t[q] * a.k + j];
+                if (r >= 0) __builtin_nontemporal_store(v[q], &rows[r * rs + u[q]]);
+            }
         }
     }
 }

@@ -108,68 +108,59 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void* __restr
         const bool bad = field == 255;                     // Inf or NaN in the block
         const uint32_t sb = bad ? 255u : (uint32_t)max(field - 2, 0);
         const uint32_t c = encode8<DT>(w, __uint_as_float(sb << 23));
-        *reinterpret_cast<uint32_t*>(codes + i * 4) = bad ? 0u : c;
+        __builtin_nontemporal_store(bad ? 0u : c, reinterpret_cast<uint32_t*>(codes + i * 4));
         if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)sb;
     }
 }
 
+// Piece i: 16 bytes of output (eight 16-bit or four fp32 values), per_row pieces a row.
 template <int DT, bool FLAT, bool VECTOR>
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t pieces,
                                                                int per_row, void* __restrict__ out, int64_t os) {
+    constexpr int N = DT == kF32 ? 4 : 8;
     const int64_t stride = (int64_t)gridDim.x * 256;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += stride) {
-        int64_t el = i * 8;
+        int64_t el = i * N;
         if (!FLAT) {
             const int64_t r = i / per_row;
-            el = r * os + (i - r * per_row) * 8;
+            el = r * os + (i - r * per_row) * N;
         }
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + i * 4);
-        const float s = __uint_as_float((uint32_t)scales[i >> 2] << 23);
-        if constexpr (DT == kBF16) {
-            const bf16x2_t v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0),
-                                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1),
-                                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2),
-                                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3)};
-            uint16_t* dst = static_cast<uint16_t*>(out) + el;
-            if constexpr (VECTOR) {
-                *reinterpret_cast<u32x4_t*>(dst) =
-                    u32x4_t{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
-                            __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    dst[2 * q] = (uint16_t)(__builtin_bit_cast(uint32_t, v[q]) & 0xFFFFu);
-                    dst[2 * q + 1] = (uint16_t)(__builtin_bit_cast(uint32_t, v[q]) >> 16);
-                }
-            }
+        const float s = __uint_as_float((uint32_t)scales[i / (kMx / N)] << 23);
+        uint32_t w[4];                                     // the piece's bits
+        if constexpr (DT == kF32) {
+            const uint32_t c = *reinterpret_cast<const uint16_t*>(codes + i * 2);
+            const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+            const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+            w[0] = __float_as_uint(a[0]); w[1] = __float_as_uint(a[1]);
+            w[2] = __float_as_uint(b[0]); w[3] = __float_as_uint(b[1]);
         } else {
-            const f32x2_t v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0),
-                                  __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1),
-                                  __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2),
-                                  __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3)};
-            if constexpr (DT == kF32) {
-                float* dst = static_cast<float*>(out) + el;
-                if constexpr (VECTOR) {
-                    *reinterpret_cast<f32x4_t*>(dst) = f32x4_t{v[0][0], v[0][1], v[1][0], v[1][1]};
-                    *reinterpret_cast<f32x4_t*>(dst + 4) = f32x4_t{v[2][0], v[2][1], v[3][0], v[3][1]};
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = v[q / 2][q & 1];
-                }
+            const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + i * 4);
+            if constexpr (DT == kBF16) {
+                w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
+                w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
+                w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
+                w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
             } else {
-                uint16_t* dst = static_cast<uint16_t*>(out) + el;
-                uint32_t h[8];
+                // through fp32: rounded to f16 once
+                const f32x2_t v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0),
+                                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1),
+                                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2),
+                                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3)};
 #pragma unroll
-                for (int q = 0; q < 8; ++q) h[q] = f32_to_f16_bits(v[q / 2][q & 1]);
-                if constexpr (VECTOR) {
-                    *reinterpret_cast<u32x4_t*>(dst) = u32x4_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16),
-                                                               h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = (uint16_t)h[q];
-                }
+                for (int q = 0; q < 4; ++q) w[q] = f32_to_f16_bits(v[q][0]) | (f32_to_f16_bits(v[q][1]) << 16);
             }
+        }
+        // streaming stores of consecutive lanes' consecutive 16 bytes
+        if constexpr (VECTOR) {
+            __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]},
+                                        reinterpret_cast<u32x4_t*>(static_cast<char*>(out) + el * (16 / N)));
+        } else if constexpr (DT == kF32) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) static_cast<uint32_t*>(out)[el + q] = w[q];
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) static_cast<uint16_t*>(out)[el + q] = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
         }
     }
 }
@@ -198,13 +189,14 @@ static void quantize_dt(const void* x, int64_t R, int C, int64_t xs, uint8_t* co
 template <int DT>
 static void dequantize_dt(const uint8_t* codes, const uint8_t* scales, int64_t R, int C, void* out, int64_t os,
                           hipStream_t s) {
-    const int64_t pieces = R * (C / 8);
+    constexpr int n = DT == kF32 ? 4 : 8;
+    const int64_t pieces = R * (C / n);
     const dim3 grid(piece_blocks(pieces));
     const int eb = dtype_bytes(DT);
     const bool v = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && (R == 1 || os * eb % 16 == 0);
     const bool flat = R == 1 || os == C;
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, codes, scales, pieces, C / 8, out, os);
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, codes, scales, pieces, C / n, out, os);
     };
     if (v) flat ? run(mxfp4_dequantize_kernel<DT, true, true>) : run(mxfp4_dequantize_kernel<DT, false, true>);
     else flat ? run(mxfp4_dequantize_kernel<DT, true, false>) : run(mxfp4_dequantize_kernel<DT, false, false>);
