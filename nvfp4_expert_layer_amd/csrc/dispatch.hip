@@ -147,9 +147,13 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a, int 
         for (int e = tid; e < L; e += kThreads) before[e] = base[e] = 0;
         __syncthreads();
         const int n = a.T * a.k;
-        for (int q = tid; q < n; q += kThreads) {
-            const int e = local_expert(a, q);
-            if (e >= 0) atomicAdd(q < p0 ? &before[e] : &base[e], 1);
+        for (int q0 = tid; q0 < n; q0 += 8 * kThreads) {    // eight loads in flight
+            int e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = q0 + i * kThreads < n ? local_expert(a, q0 + i * kThreads) : -1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (e[i] >= 0) atomicAdd(q0 + i * kThreads < p0 ? &before[e[i]] : &base[e[i]], 1);
         }
     }
     int mine = -1;
@@ -184,24 +188,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a, int 
     U* rows = static_cast<U*>(a.rows);
     const int per = (units + gridDim.y - 1) / gridDim.y, u0 = blockIdx.y * per, nu = min(per, units - u0);
     if (nu <= 0) return;
-    // four units a thread at a time: their loads first, then each one's k stores
-    for (int i0 = tid; i0 < nt * nu; i0 += 4 * kThreads) {
-        U v[4];
-        int t[4], u[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = i0 + q * kThreads;
-            t[q] = i / nu;
-            u[q] = u0 + (i - t[q] * nu);
-            if (i < nt * nu) v[q] = x[(t0 + t[q]) * xs + u[q]];
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (i0 + q * kThreads >= nt * nu) break;
-            for (int j = 0; j < a.k; ++j) {
-                const int r = dest[t[q] * a.k + j];
-                if (r >= 0) __builtin_nontemporal_store(v[q], &rows[r * rs + u[q]]);
-            }
+    for (int i = tid; i < nt * nu; i += kThreads) {
+        const int t = i / nu, u = u0 + (i - t * nu);
+        const U v = x[(t0 + t) * xs + u];
+        for (int j = 0; j < a.k; ++j) {
+            const int r = dest[t * a.k + j];
+            if (r >= 0) __builtin_nontemporal_store(v, &rows[r * rs + u]);
         }
     }
 }
@@ -257,7 +249,7 @@ static void dispatch_units(const DispatchArgs& a, const DispatchPlan& p, hipStre
     const int eb = dtype_bytes(a.dtype), per = (int)sizeof(U) / eb;
     const int units = a.x ? a.d / per : 0;
     // few blocks: the columns over several too, at least 64 units each
-    const int want = p.one_launch ? 256 : 2048, most = (units + 63) / 64;
+    const int want = p.one_launch ? 256 : 512, most = (units + 63) / 64;
     int split = want / p.blocks;
     split = split > most ? most : split;
     if (split < 1) split = 1;
