@@ -11,7 +11,7 @@
 //                      decodes its weight operand in registers (one conversion a
 //                      pair, the block scale within it), then 32x32x16 bf16 MFMAs.
 //   grad_tile_kernel   backward: the reduction runs over the weight's rows, 64 a
-//                      stage; a lane takes four neighbouring columns of eight rows,
+//                      stage; a lane takes two neighbouring columns of eight rows,
 //                      decodes them and regroups the pairs by column.
 //
 // Lane layout of the 32x32 MFMAs: lane l holds row (column) l % 32 and the K slice of
@@ -722,7 +722,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     if (t.g < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int r32 = lane & 31;
-    const int wt = wave >> 1, wk = wave & 1;             // rows 64 wt .. +64, columns 128 wk .. +128
+    const int wt = wave >> 2, wk = wave & 3;             // rows 128 wt .. +128, columns 64 wk .. +64
     const int KB = p.K / 32, kb0 = t.nt * 8, nn = (p.N + 63) / 64;
 
     // dout: four loads of 8 rows a wave and stage; codes: one of 8 weight rows x 128
@@ -783,15 +783,15 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
         asm volatile("ds_write_b16 %0, %1" ::"v"(at), "v"(b << 7) : "memory");
     };
 
-    f32x16_t acc[4][2];
+    f32x16_t acc[2][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.f;
-    const int nvi = max(0, min(2, (t.re - t.rb - wt * 64 + 31) >> 5));
-    const bool cols = kb0 * 32 + wk * 128 < p.K;
+    const int nvi = max(0, min(4, (t.re - t.rb - wt * 128 + 31) >> 5));
+    const bool cols = kb0 * 32 + wk * 64 < p.K;
 
     // Stage s in slot s % 3.  Lane half h of substep q (16 n) takes rows 16 q + 8 h .. + 8.
     // Operands are read one substep ahead, a stage's first ones before the last MFMAs of
@@ -802,38 +802,34 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     auto nloop = [&](auto nv_c) {
         constexpr int NV = decltype(nv_c)::value;
         uint32_t code[2][8];
-        u32x4_t sc[2], dv[2][2];                          // by parity of the substep
+        u32x4_t sc[2], dv[2][4];                          // by parity of the substep
         int slot = 0;
         auto operands = [&](int sl, int q, auto f_c) {
             constexpr int f = decltype(f_c)::value;
             const uint8_t* D = smem + sl * kGSlot;
-            const uint8_t* C = D + kGDout + ((wk ^ h) * 64) + 2 * r32 + (16 * q + 8 * h) * 128;
+            const uint8_t* C = D + kGDout + ((wk * 32) ^ (h * 64)) + r32 + (16 * q + 8 * h) * 128;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                dv[f][i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 64 + i * 32 + r32, 2 * q + h));
-            sc[f] = *reinterpret_cast<const u32x4_t*>(D + kGDout + kGCodes + (wk * 4 + (r32 >> 3)) * kGPitch +
+                dv[f][i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 128 + i * 32 + r32, 2 * q + h));
+            sc[f] = *reinterpret_cast<const u32x4_t*>(D + kGDout + kGCodes + (wk * 2 + (r32 >> 4)) * kGPitch +
                                                       (16 * q + 8 * h) * 2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) code[f][j] = *reinterpret_cast<const uint16_t*>(C + j * 128);
+            for (int j = 0; j < 8; ++j) code[f][j] = C[j * 128];
         };
         auto mfmas = [&](auto f_c) {
             constexpr int f = decltype(f_c)::value;
-            u32x4_t op[4];
+            u32x4_t op[2];
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 const float s0 = __uint_as_float(sc[f][j / 2] << 16), s1 = __uint_as_float(sc[f][j / 2] & 0xFFFF0000u);
-                const uint32_t c0 = code[f][j], c1 = code[f][j + 1];
-                const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 0));
-                const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, s0, 1));
-                const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 0));
-                const uint32_t b1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c1, s1, 1));
-                op[0][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
-                op[1][j / 2] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
-                op[2][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
-                op[3][j / 2] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+                const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[f][j], s0, 0));
+                const uint32_t b =
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[f][j + 1], s1, 0));
+                op[0][j / 2] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+                op[1][j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
         };
@@ -877,21 +873,23 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     issue_scales(min(3, nn - 1), 0);
     switch (cols ? nvi : 0) {
+        case 4: nloop(std::integral_constant<int, 4>{}); break;
+        case 3: nloop(std::integral_constant<int, 3>{}); break;
         case 2: nloop(std::integral_constant<int, 2>{}); break;
         case 1: nloop(std::integral_constant<int, 1>{}); break;
         default: nloop(std::integral_constant<int, 0>{}); break;
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    // operand row i of MFMA c holds column 4 i + c: value v of the four c are four
+    // operand row i of MFMA c holds column 2 i + c: values v, v + 1 of both c are four
     // consecutive columns
     if (cols) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             if (i >= nvi) break;
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-                stage4(p, smem, t, wt * 64 + i * 32 + r32, wk * 128 + 4 * (8 * (v >> 2) + 4 * h + (v & 3)), p.K,
-                       acc[0][i][v], acc[1][i][v], acc[2][i][v], acc[3][i][v]);
+            for (int v = 0; v < 16; v += 2)
+                stage4(p, smem, t, wt * 128 + i * 32 + r32, wk * 64 + 2 * (8 * (v >> 2) + 4 * h + (v & 3)), p.K,
+                       acc[0][i][v], acc[1][i][v], acc[0][i][v + 1], acc[1][i][v + 1]);
         }
     }
     store_staged(p, smem, t, p.K);
