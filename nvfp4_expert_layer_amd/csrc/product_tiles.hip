@@ -501,9 +501,10 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
 // ---------------------------------------------------------------------------
 constexpr int kARows = 256 * 128;                        // 64 k of the tile's bf16 rows (32 KB)
 constexpr int kAWeight = 256 * 64;                        // 128 k of the weight's codes
-constexpr int a16_chunk(bool aligned) { return kAWeight + scale_bytes(aligned, 4); }
-constexpr int kAOffW = 3 * kARows;                       // LDS: rows [3] | weight [3]
-constexpr int a16_lds(bool aligned) { return kAOffW + 3 * a16_chunk(aligned); }   // 147 or 156 KB
+// LDS: rows [3] | codes [3] | scales [2], each 256 k of them: loading them 128 k at a time
+// took as many line accesses as the rows (a row's few bytes are a line of their own)
+constexpr int kAOffW = 3 * kARows, kAOffS = kAOffW + 3 * kAWeight;
+constexpr int a16_lds(bool aligned) { return kAOffS + 2 * scale_bytes(aligned, 8); }   // 148 or 160 KB
 
 __device__ __forceinline__ f32x16_t mfma_bf16_32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
@@ -512,7 +513,7 @@ __device__ __forceinline__ f32x16_t mfma_bf16_32(const u32x4_t& a, const u32x4_t
 
 template <bool ALIGNED>
 __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
-    constexpr int kAChunk = a16_chunk(ALIGNED);
+    constexpr int kScales = scale_bytes(ALIGNED, 8);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const Tile t = find_tile(p, (p.N + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
     if (t.g < 0) return;
@@ -527,9 +528,9 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     const uint16_t* abase = static_cast<const uint16_t*>(p.a) + (int64_t)t.rb * p.as;
     auto wrow = [&](int r) { return (uint32_t)min(r, p.N - 1 - n0); };
 
-    // rows: four loads of 1 KB (8 rows of 128 bytes) a wave and step; weight codes: two
-    // of 1 KB (16 rows of 64 bytes) a wave and chunk; scales: 64 rows' dwords, each
-    // quarter by two waves (the same bytes), or two of a row's four bytes a wave
+    // rows: four loads of 1 KB (8 rows of 128 bytes) a wave and step; codes: two of 1 KB
+    // (16 rows of 64 bytes) a wave and chunk of 128 k; scales, every 256 k: 32 rows' two
+    // dwords a wave, or (not ALIGNED) each of their eight bytes to a dword
     uint32_t aoff[4];
     int au[4];
 #pragma unroll
@@ -546,7 +547,11 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
         cu[q] = (lane & 3) ^ (((r >> 1) ^ (r >> 3)) & 3);
         coff[q] = wrow(r) * (uint32_t)(p.K / 2) + cu[q] * 16;
     }
-    const uint32_t soff = wrow((wave & 3) * 64 + lane) * (uint32_t)KB;
+    constexpr int kSLoads = ALIGNED ? 1 : 4, kSLanes = ALIGNED ? 2 : 8;      // lanes a row
+    uint32_t soff[kSLoads];
+    const int sb = (lane & (kSLanes - 1)) * (8 / kSLanes);
+#pragma unroll
+    for (int q = 0; q < kSLoads; ++q) soff[q] = wrow(wave * 32 + q * 8 + lane / kSLanes) * (uint32_t)KB + sb;
 
     auto issue_rows = [&](int ks, int slot) {
         uint8_t* base = smem + slot * kARows + wave * 4096;
@@ -559,9 +564,9 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
             for (int q = 0; q < 4; ++q) to_lds16(within(ks * 8 + au[q] < KB * 4, ab + aoff[q]), base + q * 1024);
         }
     };
-    auto issue_weight = [&](int c, int slot) {
-        uint8_t* base = smem + kAOffW + slot * kAChunk;
-        const uint8_t *wb = scalar(wbase + (int64_t)c * 64), *sb = scalar(sbase + (int64_t)c * 4);
+    auto issue_codes = [&](int c, int slot) {
+        uint8_t* base = smem + kAOffW + slot * kAWeight;
+        const uint8_t* wb = scalar(wbase + (int64_t)c * 64);
         if (ALIGNED || c * 4 + 4 <= KB) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) to_lds16(wb + coff[q], base + (wave * 2 + q) * 1024);
@@ -570,15 +575,15 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
             for (int q = 0; q < 2; ++q)
                 to_lds16(within(c * 4 + cu[q] < KB, wb + coff[q]), base + (wave * 2 + q) * 1024);
         }
-        if (ALIGNED) {
-            to_lds4(sb + soff, base + kAWeight + (wave & 3) * 256);
-        } else {
+    };
+    auto issue_scales = [&](int c, int slot) {            // c: of 256 k
+        uint8_t* base = smem + kAOffS + slot * kScales + wave * (kScales / kTWaves);
+        const uint8_t* src = scalar(sbase + (int64_t)c * 8);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int b = (wave >> 2) * 2 + i;
-                to_lds1(within(c * 4 + b < KB, sb + b + soff),
-                        base + kAWeight + b * 1024 + (wave & 3) * 256);
-            }
+        for (int q = 0; q < kSLoads; ++q) {
+            const void* from = within(c * 8 + sb < KB, src + soff[q]);
+            if (ALIGNED) to_lds4(from, base);
+            else to_lds1(from, base + q * 256);
         }
     };
 
@@ -593,13 +598,14 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     const bool cols = n0 + wn * 64 < p.N;
     const int r32 = lane & 31;
 
-    // Step ks: rows in slot ks % 3, chunk ks / 2 in weight slot (ks / 2) % 3.  Lane half h
-    // of MFMA kk (0 .. 3) takes k = 32 h + 8 kk .. + 8 of the step: dword kk of the weight
-    // row's unit 2 (ks % 2) + h, and the row's unit 4 h + kk.  Operands are read one MFMA
-    // ahead, a step's first ones before the last MFMAs of the step before.  The barrier
-    // stands there: the step's rows have been read (slot free for step ks + 3), after an
-    // odd step its chunk too (for chunk + 3), and the wait leaves in flight only what was
-    // issued since the next step's rows (past the end valid data again).
+    // Step ks: rows in slot ks % 3, codes of chunk ks / 2 in slot (ks / 2) % 3, scales in
+    // slot (ks / 4) % 2.  Lane half h of MFMA kk (0 .. 3) takes k = 32 h + 8 kk .. + 8 of the
+    // step: dword kk of the weight row's unit 2 (ks % 2) + h, and the row's unit 4 h + kk.
+    // Operands are read one MFMA ahead, a step's first ones before the last MFMAs of the
+    // step before.  The barrier stands there: the step's rows have been read (slot free for
+    // step ks + 3), after an odd step its codes (for chunk + 3), after every fourth its
+    // scales.  The wait leaves in flight only what was issued since the next step's rows:
+    // six loads or more (past the end valid data again).
     auto kloop = [&](auto nv_c) {
         constexpr int NV = decltype(nv_c)::value;
         u32x4_t wc[2][2], av[2][4];                       // codes by parity of the step; rows by parity of kk
@@ -612,15 +618,15 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
                 av[f][i] = *reinterpret_cast<const u32x4_t*>(smem + slot * kARows +
                                                              swz8(wm * 128 + i * 32 + r32, 4 * h + kk));
         };
-        auto codes = [&](int slot, auto st_c) {
+        auto codes = [&](int ks, int slot, auto st_c) {
             constexpr int ST = decltype(st_c)::value;
-            const uint8_t* W = smem + kAOffW + slot * kAChunk;
+            const uint8_t* W = smem + kAOffW + slot * kAWeight;
+            const uint8_t* S = smem + kAOffS + ((ks >> 2) & 1) * kScales + (2 * (ks & 3) + h) * (ALIGNED ? 1 : 4);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int r = wn * 64 + j * 32 + r32, b = 2 * ST + h;
-                wc[ST][j] = *reinterpret_cast<const u32x4_t*>(W + swz4(r, b));
-                const uint32_t sb = W[kAWeight + (ALIGNED ? r * 4 + b : b * 1024 + r * 4)];
-                sc[ST][j] = __uint_as_float(sb << 23);
+                const int r = wn * 64 + j * 32 + r32;
+                wc[ST][j] = *reinterpret_cast<const u32x4_t*>(W + swz4(r, 2 * ST + h));
+                sc[ST][j] = __uint_as_float((uint32_t)S[r * (kScales / 256)] << 23);
             }
         };
         auto mfmas = [&](auto st_c, int kk, auto f_c) {
@@ -650,12 +656,12 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
                 mfmas(st_c, 2, c0);
             }
             keep_order();
-            if (ALIGNED) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             issue_rows(min(ks + 3, nk - 1), as);
-            if (ST == 1) issue_weight(min(ks / 2 + 3, nc - 1), ws);
+            if (ST == 1) issue_codes(min(ks / 2 + 3, nc - 1), ws);
+            if (ST == 1 && (ks & 3) == 3) issue_scales(min(ks / 4 + 2, (nc - 1) / 2), (ks >> 2) & 1);
             if constexpr (NV > 0) {
-                codes(ST == 1 ? wnx : ws, next_c);
+                codes(ks + 1, ST == 1 ? wnx : ws, next_c);
                 rows(an, 0, c0);
                 keep_order();
                 mfmas(st_c, 3, c1);
@@ -664,7 +670,7 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
             if (ST == 1) ws = wnx;
         };
         if constexpr (NV > 0) {
-            codes(0, c0);
+            codes(0, 0, c0);
             rows(0, 0, c0);
         }
         for (int ks = 0; ks < nk; ks += 2) {
@@ -675,7 +681,8 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         issue_rows(min(i, nk - 1), i);
-        issue_weight(min(i, nc - 1), i);
+        issue_codes(min(i, nc - 1), i);
+        if (i < 2) issue_scales(min(i, (nc - 1) / 2), i);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     switch (cols ? nvi : 0) {
