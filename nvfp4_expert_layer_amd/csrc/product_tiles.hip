@@ -250,9 +250,12 @@ __device__ __forceinline__ Tile table_tile(const ProductArgs& p, const int* tabl
                 logical - tile * NT};
 }
 
-// A wave's 32 tokens x 32 outputs (an accumulator) to memory through 2 KB of LDS of its
-// own, without a barrier: tokens' 64-byte rows, whose 16-byte units trade places by row
-// so that both the 8-byte stores and the 16-byte loads spread over all banks.
+// A wave's 32 tokens x 32 outputs to memory through 2 KB of LDS of its own, without a
+// barrier: tokens' 64-byte rows, whose 16-byte units trade places by row so that both the
+// 8-byte stores and the 16-byte loads spread over all banks.  The lane's four values 4 g
+// .. + 4 are outputs 8 g + 4 h .. + 4 (an accumulator), or, PAIRED, 16 (g / 2) + 8 h + 4 (g
+// % 2) .. + 4 (the backward's column pairs).
+template <bool PAIRED>
 __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage, const Tile& t, int row0, int col0,
                                            int width, const f32x16_t& acc, bool vec) {
     const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
@@ -260,10 +263,11 @@ __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage,
     if (p.out_dtype == kF32) {
         if (t.rb + row0 + r32 < t.re) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                store4(p.out, kF32, (t.rb + row0 + r32) * p.os + t.nt * kTN + col0 + 8 * g + 4 * h,
-                       f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}, left - 8 * g - 4 * h,
-                       p.out_vec);
+            for (int g = 0; g < 4; ++g) {
+                const int c = PAIRED ? 16 * (g >> 1) + 8 * h + 4 * (g & 1) : 8 * g + 4 * h;
+                store4(p.out, kF32, (t.rb + row0 + r32) * p.os + t.nt * kTN + col0 + c,
+                       f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}, left - c, p.out_vec);
+            }
         }
         return;
     }
@@ -275,7 +279,8 @@ __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage,
         else
             v = u32x2_t{f32_to_f16_bits(acc[4 * g]) | (f32_to_f16_bits(acc[4 * g + 1]) << 16),
                         f32_to_f16_bits(acc[4 * g + 2]) | (f32_to_f16_bits(acc[4 * g + 3]) << 16)};
-        const uint32_t at = lds_offset(stage) + r32 * 64 + ((g ^ (r32 >> 2)) & 3) * 16 + h * 8;
+        const int unit = PAIRED ? 2 * (g >> 1) + h : g, half = PAIRED ? g & 1 : h;
+        const uint32_t at = lds_offset(stage) + r32 * 64 + ((unit ^ (r32 >> 2)) & 3) * 16 + half * 8;
         // written out: before an ordinary LDS store the compiler waits for every direct
         // load in flight.  LDS serves a wave in order: the loads below come after.
         asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(v) : "memory");
@@ -488,7 +493,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
             if (i >= nvi) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                wave_store(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i], vec);
+                wave_store<false>(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i], vec);
         }
         mine += stride;
         if (!ALIGNED || mine >= end) break;
@@ -713,193 +718,198 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
 // ---------------------------------------------------------------------------
 constexpr int kGDout = 256 * 128;                        // 64 n of the tile's bf16 gradient rows (32 KB)
 constexpr int kGCodes = 64 * 128;                        // 64 weight rows, 256 k (8 KB)
-constexpr int kGPitch = 144;                             // scales: [8 blocks][64 rows] as the upper halves of
-constexpr int kGScales = 8 * kGPitch;                    //   fp32 powers of two; the pitch spreads the banks
+constexpr int kGScales = 64 * 8 * 4;                     // their scales, a byte in a dword each
 constexpr int kGSlot = kGDout + kGCodes + kGScales;
-constexpr int kGOffRaw = 3 * kGSlot, kGRaw = 512 * 4;    // scale bytes as loaded, a dword each, three stages
-constexpr int kGLds = kGOffRaw + 3 * kGRaw;              // 130 KB (the output's staging: 132 KB)
-constexpr int kGLdsAll = kGLds > kTM * kYS * 2 ? kGLds : kTM * kYS * 2;
+constexpr int kGOffStage = 3 * kGSlot, kGOffTable = kGOffStage + kTWaves * kWaveStage;
+constexpr int kGLds = kGOffTable + kTable;               // stages [3] | waves' staging [8] | table: 147 KB
 
-// VECTOR: dout's rows in 16-byte units (dout_vector), else element by element
-// through registers.
+// Tiles one after another, as in mx_tile_kernel.  VECTOR: dout's rows in 16-byte units
+// (dout_vector), else element by element through registers.
 template <bool VECTOR>
 __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const Tile t = find_tile(p, (p.K + kTN - 1) / kTN, reinterpret_cast<int*>(smem));
-    if (t.g < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
-    const int r32 = lane & 31;
-    const int wt = wave >> 2, wk = wave & 3;             // rows 128 wt .. +128, columns 64 wk .. +64
-    const int KB = p.K / 32, kb0 = t.nt * 8, nn = (p.N + 63) / 64;
+    const int r32 = lane & 31, wt = wave >> 2, wk = wave & 3;    // rows 128 wt .. +128, columns 64 wk .. +64
+    const int NT = (p.K + kTN - 1) / kTN, KB = p.K / 32, nn = (p.N + 63) / 64;
+    const bool vec = p.os % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+    int* table = reinterpret_cast<int*>(smem + kGOffTable);
+    const int all = tile_table(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
+    const int end = min(((int)blockIdx.x & 7) * per + per, all);
+    int mine = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+    if (mine >= end) return;
+    Tile t = table_tile(p, table, mine, NT);
 
+    // ---- loads, three stages ahead ----
     // dout: four loads of 8 rows a wave and stage; codes: one of 8 weight rows x 128
     // bytes, whose two 64-byte halves trade places in every other group of 8 rows (the
-    // two lane halves read rows 8 apart: different banks); scales: one byte a thread
-    const uint16_t* dbase = static_cast<const uint16_t*>(p.a) + (int64_t)t.rb * p.as;
+    // two lane halves read rows 8 apart: different banks); scales: wave w's rows 8 w .. +8,
+    // lane i block i / 8 of row i % 8, so that eight rows' scales of a block follow each
+    // other.  Columns past K, rows past N: zeros.
+    const uint16_t* dbase;
+    const uint8_t *cbase, *sbase;
     uint32_t doff[4];
-    int du[4];
+    bool cin, sin;
+    const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ ((wave & 1) << 2), srow = wave * 8 + (lane & 7);
+    const uint32_t coff = crow * (uint32_t)(p.K / 2) + cunit * 16, soff = srow * (uint32_t)KB + (lane >> 3);
+    const int du = (lane & 7) ^ (lane >> 3);
+    auto load_from = [&](const Tile& n) {
+        dbase = static_cast<const uint16_t*>(p.a) + (int64_t)n.rb * p.as;
+        cbase = p.w + (int64_t)n.g * p.N * (p.K / 2) + n.nt * 128;
+        sbase = p.w_s + (int64_t)n.g * p.N * KB + n.nt * 8;
+        cin = n.nt * 8 + cunit < KB;
+        sin = n.nt * 8 + (lane >> 3) < KB;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int r = (wave * 4 + q) * 8 + (lane >> 3);
-        du[q] = (lane & 7) ^ (lane >> 3) ^ (q & 1);
-        doff[q] = (uint32_t)(min(r, t.re - 1 - t.rb) * p.as + du[q] * 8);
-    }
-    // (columns past K: zeros at every stage)
-    const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ ((wave & 1) << 2);
-    const bool cin = kb0 + cunit < KB;
-    const uint8_t* cbase = p.w + (int64_t)t.g * p.N * (p.K / 2) + kb0 * 16;
-    const uint32_t coff = crow * (uint32_t)(p.K / 2) + cunit * 16;
-    const int srow = tid >> 3, sblk = tid & 7;
-    const bool sin = kb0 + sblk < KB;
-    const uint8_t* sbase = p.w_s + (int64_t)t.g * p.N * KB + kb0;
-    const uint32_t soff = srow * (uint32_t)KB + sblk;
-
-    auto issue = [&](int s, int slot) {
-        uint8_t* base = smem + slot * kGSlot + wave * 4096;
-        const uint16_t* db = scalar(dbase + s * 64);
-        const uint8_t* cs = scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff;
-        uint8_t* cd = smem + slot * kGSlot + kGDout + wave * 1024;
-        if (s * 64 + 64 <= p.N) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (VECTOR) to_lds16(db + doff[q], base + q * 1024);
-                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], 8);
-            }
-            to_lds16(within(cin, cs), cd);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int left = p.N - s * 64 - du[q] * 8;
-                if (VECTOR) to_lds16(within(left > 0, db + doff[q]), base + q * 1024);
-                else *reinterpret_cast<u32x4_t*>(base + q * 1024 + lane * 16) = load8_bf16<false>(db + doff[q], left);
-            }
-            to_lds16(within(cin && s * 64 + crow < p.N, cs), cd);
+        for (int q = 0; q < 4; ++q) {
+            const int r = (wave * 4 + q) * 8 + (lane >> 3);
+            doff[q] = (uint32_t)(min(r, n.re - 1 - n.rb) * p.as + (du ^ (q & 1)) * 8);
         }
     };
-    // scales: byte tid of a stage (row tid / 8, block tid % 8) to a dword of its own
-    auto issue_scales = [&](int s, int slot) {
+    auto issue = [&](int s, int slot) {
+        uint8_t* base = smem + slot * kGSlot;
+        const uint16_t* db = scalar(dbase + s * 64);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint8_t* dst = base + (wave * 4 + q) * 1024;
+            const int left = p.N - s * 64 - (du ^ (q & 1)) * 8;
+            if (VECTOR) to_lds16(within(left > 0, db + doff[q]), dst);
+            else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16<false>(db + doff[q], left);
+        }
+        to_lds16(within(cin && s * 64 + crow < p.N, scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff),
+                 base + kGDout + wave * 1024);
         to_lds1(within(sin && s * 64 + srow < p.N, scalar(sbase + (int64_t)s * 64 * KB) + soff),
-                smem + kGOffRaw + slot * kGRaw + wave * 256);
+                base + kGDout + kGCodes + wave * 256);
     };
-    // and from there to where the operands are decoded
-    auto put_scales = [&](int slot) {
-        const uint32_t b = smem[kGOffRaw + slot * kGRaw + tid * 4];
-        const uint32_t at = lds_offset(smem) + slot * kGSlot + kGDout + kGCodes + sblk * kGPitch + srow * 2;
-        // written out: before an ordinary LDS store the compiler waits for every direct
-        // load in flight (they write LDS too).  The step's own wait covers it.
-        asm volatile("ds_write_b16 %0, %1" ::"v"(at), "v"(b << 7) : "memory");
+    int next = mine, is = 0;                             // tile and stage of the next loads
+    bool more = true;
+    auto advance = [&]() {
+        if (++is < nn) return;
+        is = 0;
+        next += stride;
+        more = next < end;
+        if (more) load_from(table_tile(p, table, next, NT));
     };
 
+    // ---- the multiplication ----
+    // Lane half h of substep q (16 n) takes weight rows 16 q + 8 h .. + 8 of the stage, two
+    // neighbouring columns of each: MFMA c's operand row i is column 2 i + c.  Substep q + 1
+    // is read from LDS before the MFMAs of substep q and decoded between them.
     f32x16_t acc[2][4];
+    u32x4_t op[2][2], dv[2][4];                          // operands by parity of the substep
+    uint32_t code[8];                                    // the next substep's codes and scales
+    u32x4_t sc[2];
+    auto read = [&](int sl, int q, auto f_c) {
+        constexpr int f = decltype(f_c)::value;
+        const uint8_t* D = smem + sl * kGSlot;
+        const uint8_t* C = D + kGDout + ((wk * 32) ^ (h * 64)) + r32 + (16 * q + 8 * h) * 128;
+        const uint8_t* S = D + kGDout + kGCodes + (2 * q + h) * 256 + (wk * 2 + (r32 >> 4)) * 32;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+        for (int j = 0; j < 8; ++j) code[j] = C[j * 128];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sc[i] = *reinterpret_cast<const u32x4_t*>(S + 16 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
+            dv[f][i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 128 + i * 32 + r32, 2 * q + h));
+    };
+    auto decode = [&](int j, auto f_c) {                 // weight rows j and j + 1 of the eight
+        constexpr int f = decltype(f_c)::value;
+        const float s0 = __uint_as_float(sc[j / 4][j & 3] << 23);
+        const float s1 = __uint_as_float(sc[j / 4][(j & 3) + 1] << 23);
+        const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[j], s0, 0));
+        const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[j + 1], s1, 0));
+        op[f][0][j / 2] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+        op[f][1][j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    };
+    // MFMAs of parity f, the other parity's decoding between them; FULL: four row blocks
+    auto mfmas = [&](auto full_c, int nv, auto f_c, auto g_c) {
+        constexpr bool FULL = decltype(full_c)::value;
+        constexpr int f = decltype(f_c)::value;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.f;
-    const int nvi = max(0, min(4, (t.re - t.rb - wt * 128 + 31) >> 5));
-    const bool cols = kb0 * 32 + wk * 64 < p.K;
-
-    // Stage s in slot s % 3.  Lane half h of substep q (16 n) takes rows 16 q + 8 h .. + 8.
-    // Operands are read one substep ahead, a stage's first ones before the last MFMAs of
-    // the stage before; the barrier stands there, after which the stage's slot is free for
-    // stage s + 3 and the wait has left only the last step's loads in flight.  A stage's
-    // scales are loaded one step earlier than its rest and rearranged in the step before
-    // its own, ahead of that step's barrier.
-    auto nloop = [&](auto nv_c) {
-        constexpr int NV = decltype(nv_c)::value;
-        uint32_t code[2][8];
-        u32x4_t sc[2], dv[2][4];                          // by parity of the substep
-        int slot = 0;
-        auto operands = [&](int sl, int q, auto f_c) {
-            constexpr int f = decltype(f_c)::value;
-            const uint8_t* D = smem + sl * kGSlot;
-            const uint8_t* C = D + kGDout + ((wk * 32) ^ (h * 64)) + r32 + (16 * q + 8 * h) * 128;
+        for (int i = 0; i < 4; ++i) {
+            if (FULL || i < nv) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                dv[f][i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 128 + i * 32 + r32, 2 * q + h));
-            sc[f] = *reinterpret_cast<const u32x4_t*>(D + kGDout + kGCodes + (wk * 2 + (r32 >> 4)) * kGPitch +
-                                                      (16 * q + 8 * h) * 2);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) code[f][j] = C[j * 128];
-        };
-        auto mfmas = [&](auto f_c) {
-            constexpr int f = decltype(f_c)::value;
-            u32x4_t op[2];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float s0 = __uint_as_float(sc[f][j / 2] << 16), s1 = __uint_as_float(sc[f][j / 2] & 0xFFFF0000u);
-                const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[f][j], s0, 0));
-                const uint32_t b =
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[f][j + 1], s1, 0));
-                op[0][j / 2] = __builtin_amdgcn_perm(b, a, 0x05040100u);
-                op[1][j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < NV; ++i) acc[c][i] = mfma_bf16_32(op[c], dv[f][i], acc[c][i]);
-        };
-        const std::integral_constant<int, 0> c0;
-        const std::integral_constant<int, 1> c1;
-        if constexpr (NV > 0) operands(0, 0, c0);
-        for (int s = 0; s < nn; ++s) {
-            const int next = slot == 2 ? 0 : slot + 1;
-            put_scales(next);
-            if constexpr (NV > 0) {
-                operands(slot, 1, c1);
-                keep_order();
-                mfmas(c0);
-                operands(slot, 2, c0);
-                keep_order();
-                mfmas(c1);
-                operands(slot, 3, c1);
-                keep_order();
-                mfmas(c0);
+                for (int c = 0; c < 2; ++c) acc[c][i] = mfma_bf16_32(op[f][c], dv[f][i], acc[c][i]);
             }
             keep_order();
-            if (VECTOR) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            issue(min(s + 3, nn - 1), slot);
-            issue_scales(min(s + 4, nn - 1), next);
-            if constexpr (NV > 0) {
-                operands(next, 0, c0);
-                keep_order();
-                mfmas(c1);
-            }
-            slot = next;
+            if (i > 0) decode(2 * (i - 1), g_c);
+            if (i == 3) decode(6, g_c);
+            keep_order();
         }
     };
+    const std::integral_constant<int, 0> c0;
+    const std::integral_constant<int, 1> c1;
+    // The barrier stands before a stage's last MFMAs: its slot has been read (free for the
+    // stage three on), and the wait has left only the last step's loads in flight.
+    int slot = 0;
+    auto stages = [&](auto full_c, int nv) {             // nv: 32-row blocks of this wave with rows
+        for (int s = 0; s < nn; ++s) {
+            const int following = slot == 2 ? 0 : slot + 1;
+            read(slot, 1, c1);
+            keep_order();
+            mfmas(full_c, nv, c0, c1);
+            read(slot, 2, c0);
+            keep_order();
+            mfmas(full_c, nv, c1, c0);
+            read(slot, 3, c1);
+            keep_order();
+            mfmas(full_c, nv, c0, c1);
+            // (a workgroup's last stages issue nothing: then every load is waited for)
+            if (!more) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else if (VECTOR) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (more) {
+                issue(is, slot);
+                advance();
+            }
+            read(following, 0, c0);
+            keep_order();
+            mfmas(full_c, nv, c1, c0);
+            slot = following;
+        }
+    };
+    load_from(t);
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
-        issue(min(s, nn - 1), s);
-        issue_scales(min(s, nn - 1), s);
+        if (!more) continue;
+        issue(is, s);
+        advance();
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    put_scales(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    issue_scales(min(3, nn - 1), 0);
-    switch (cols ? nvi : 0) {
-        case 4: nloop(std::integral_constant<int, 4>{}); break;
-        case 3: nloop(std::integral_constant<int, 3>{}); break;
-        case 2: nloop(std::integral_constant<int, 2>{}); break;
-        case 1: nloop(std::integral_constant<int, 1>{}); break;
-        default: nloop(std::integral_constant<int, 0>{}); break;
-    }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    // operand row i of MFMA c holds column 2 i + c: values v, v + 1 of both c are four
-    // consecutive columns
-    if (cols) {
+    read(0, 0, c0);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) decode(j, c0);
+    for (;;) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[c][i][v] = 0.f;
+        const bool cols = t.nt * kTN + wk * 64 < p.K;
+        const int nvi = cols ? max(0, min(4, (t.re - t.rb - wt * 128 + 31) >> 5)) : 0;
+        if (nvi == 4) stages(std::true_type{}, 4);
+        else stages(std::false_type{}, nvi);
+        // values v, v + 1 of both operands are four consecutive columns: 64 columns by 32
+        // rows as two staged blocks of 32
+        uint8_t* stage = smem + kGOffStage + wave * kWaveStage;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= nvi) break;
 #pragma unroll
-            for (int v = 0; v < 16; v += 2)
-                stage4(p, smem, t, wt * 128 + i * 32 + r32, wk * 64 + 2 * (8 * (v >> 2) + 4 * h + (v & 3)), p.K,
-                       acc[0][i][v], acc[1][i][v], acc[0][i][v + 1], acc[1][i][v + 1]);
+            for (int b = 0; b < 2; ++b) {
+                // operand rows 16 b .. + 16 (values 8 b .. + 8): columns 32 b .. + 32
+                f32x16_t o;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    o[2 * v] = acc[0][i][8 * b + v];
+                    o[2 * v + 1] = acc[1][i][8 * b + v];
+                }
+                wave_store<true>(p, stage, t, wt * 128 + i * 32, wk * 64 + b * 32, p.K, o, vec);
+            }
         }
+        mine += stride;
+        if (mine >= end) break;
+        t = table_tile(p, table, mine, NT);
     }
-    store_staged(p, smem, t, p.K);
 }
 
 template <auto Kern, int LDS>
@@ -924,9 +934,9 @@ hipError_t launch_product_tiles(const ProductArgs& p, int cus, hipStream_t s) {
 }
 
 hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t s) {
-    const int64_t tiles = tile_grid(p, (p.K + kTN - 1) / kTN);
-    return dout_vector(p) ? launch_tiles<grad_tile_kernel<true>, kGLdsAll>(p, tiles, s)
-                          : launch_tiles<grad_tile_kernel<false>, kGLdsAll>(p, tiles, s);
+    const int64_t grid = min(tile_grid(p, (p.K + kTN - 1) / kTN), (int64_t)max(cus / 8 * 8, 8));
+    return dout_vector(p) ? launch_tiles<grad_tile_kernel<true>, kGLds>(p, grid, s)
+                          : launch_tiles<grad_tile_kernel<false>, kGLds>(p, grid, s);
 }
 
 }  // namespace moe
