@@ -417,7 +417,7 @@ hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
 }
 
 // The tiles address 256 rows by 32-bit offsets.
-static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 23); }
+static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 
 // Rows a group (M / G, an upper bound of their mean) up to which the weight is streamed
 // past the tokens instead of multiplied in 256 x 256 tiles.  Measured on 64 groups of

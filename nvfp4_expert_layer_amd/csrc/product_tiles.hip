@@ -44,20 +44,31 @@ __device__ __forceinline__ void to_lds4(const void* src, void* dst) {
 __device__ __forceinline__ void to_lds1(const void* src, void* dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 1, 0, 0);
 }
-// A wave-uniform pointer, in scalar registers and opaque: loads then take it with a
-// 32-bit lane offset (else each load keeps and advances a 64-bit pointer a lane).
-template <typename T>
-__device__ __forceinline__ T* scalar(T* p) {
-    asm("" : "+s"(p));
-    return p;
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
+}
+
+// A direct load of BYTES a lane from a scalar base and a 32-bit lane offset to LDS
+// (lane i at dst + i * max(BYTES, 4); dst is the same for the wave).  Written out: the
+// compiler adds 64-bit addresses a lane for each load inside a loop.  M0 holds the LDS
+// address (one wait state before its use); nothing comes back to registers, and the
+// kernels' own waits cover the loads.
+template <int BYTES>
+__device__ __forceinline__ void load_lds(const void* base, uint32_t off, const void* dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_offset(dst));
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                     ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
+    else if constexpr (BYTES == 4)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                     ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
+                     ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
 }
 // Operand reads stay before the MFMAs that follow them in the source (the scheduler
 // would sink each read to its use and wait for it there).
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-    return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
-}
 
 // p, or the zeros where `in` is false, without a branch (the compiler waits for every
 // outstanding load around one).
@@ -356,22 +367,35 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     // part 0 .. 3: the wave's codes of both operands; 4: its scales
     auto issue = [&](int c, int slot, int part) {
         uint8_t* base = smem + slot * kSlot;
+        const bool whole = c * 8 + 8 <= KB;
         if (part < 4) {
-            const uint8_t* ws = scalar(wbase + (int64_t)c * 128) + coff[part];
-            const uint8_t* as = scalar(abase + (int64_t)c * 128) + aoff[part];
-            const bool in = c * 8 + (cu ^ (part & 1)) < KB;
-            to_lds16(within(in, ws), base + (wave * 4 + part) * 1024);
-            to_lds16(within(in, as), base + kMxCodes + (wave * 4 + part) * 1024);
-        } else if (ALIGNED) {
-            const bool in = c * 8 + (lane & 1) * 4 < KB;
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                to_lds4(within(in, scalar(sbase + (int64_t)c * 8) + soff[q]), base + sdst + srow * 8 + q * 256);
+            const uint8_t *wb = wbase + (int64_t)c * 128, *ab = abase + (int64_t)c * 128;
+            uint8_t *wd = base + (wave * 4 + part) * 1024, *ad = wd + kMxCodes;
+            if (whole) {
+                load_lds<16>(wb, coff[part], wd);
+                load_lds<16>(ab, aoff[part], ad);
+            } else {
+                const bool in = c * 8 + (cu ^ (part & 1)) < KB;
+                to_lds16(within(in, wb + coff[part]), wd);
+                to_lds16(within(in, ab + aoff[part]), ad);
+            }
         } else {
+            const uint8_t* sb = sbase + (int64_t)c * 8;
+            if (ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                to_lds1(within(c * 8 + i < KB, scalar(sbase + (int64_t)c * 8 + i) + soff[0]),
-                        base + sdst + i * 1024 + srow * 4);
+                for (int q = 0; q < 2; ++q) {
+                    uint8_t* sd = base + sdst + srow * 8 + q * 256;
+                    if (whole) load_lds<4>(sb, soff[q], sd);
+                    else to_lds4(within(c * 8 + (lane & 1) * 4 < KB, sb + soff[q]), sd);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint8_t* sd = base + sdst + i * 1024 + srow * 4;
+                    if (whole) load_lds<1>(sb + i, soff[0], sd);
+                    else to_lds1(within(c * 8 + i < KB, sb + i + soff[0]), sd);
+                }
+            }
         }
     };
     int next = mine, ic = 0;                             // tile and stage of the next loads
@@ -542,7 +566,7 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     for (int q = 0; q < 4; ++q) {
         const int r = (wave * 4 + q) * 8 + (lane >> 3);
         au[q] = (lane & 7) ^ (lane >> 3) ^ (q & 1);
-        aoff[q] = (uint32_t)(min(r, t.re - 1 - t.rb) * p.as + au[q] * 8);
+        aoff[q] = (uint32_t)(min(r, t.re - 1 - t.rb) * p.as + au[q] * 8) * 2;
     }
     uint32_t coff[2];
     int cu[2];
@@ -560,21 +584,23 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
 
     auto issue_rows = [&](int ks, int slot) {
         uint8_t* base = smem + slot * kARows + wave * 4096;
-        const uint16_t* ab = scalar(abase + (int64_t)ks * 64);
+        const uint16_t* ab = abase + (int64_t)ks * 64;
         if (ALIGNED || ks * 2 + 2 <= KB) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) to_lds16(ab + aoff[q], base + q * 1024);
+            for (int q = 0; q < 4; ++q) load_lds<16>(ab, aoff[q], base + q * 1024);
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) to_lds16(within(ks * 8 + au[q] < KB * 4, ab + aoff[q]), base + q * 1024);
+            for (int q = 0; q < 4; ++q)
+                to_lds16(within(ks * 8 + au[q] < KB * 4, reinterpret_cast<const uint8_t*>(ab) + aoff[q]),
+                         base + q * 1024);
         }
     };
     auto issue_codes = [&](int c, int slot) {
         uint8_t* base = smem + kAOffW + slot * kAWeight;
-        const uint8_t* wb = scalar(wbase + (int64_t)c * 64);
+        const uint8_t* wb = wbase + (int64_t)c * 64;
         if (ALIGNED || c * 4 + 4 <= KB) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) to_lds16(wb + coff[q], base + (wave * 2 + q) * 1024);
+            for (int q = 0; q < 2; ++q) load_lds<16>(wb, coff[q], base + (wave * 2 + q) * 1024);
         } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -583,12 +609,17 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
     };
     auto issue_scales = [&](int c, int slot) {            // c: of 256 k
         uint8_t* base = smem + kAOffS + slot * kScales + wave * (kScales / kTWaves);
-        const uint8_t* src = scalar(sbase + (int64_t)c * 8);
+        const uint8_t* src = sbase + (int64_t)c * 8;
+        const bool whole = c * 8 + 8 <= KB;
 #pragma unroll
         for (int q = 0; q < kSLoads; ++q) {
-            const void* from = within(c * 8 + sb < KB, src + soff[q]);
-            if (ALIGNED) to_lds4(from, base);
-            else to_lds1(from, base + q * 256);
+            if (whole) {
+                load_lds<ALIGNED ? 4 : 1>(src, soff[q], base + q * 256);
+            } else {
+                const void* from = within(c * 8 + sb < KB, src + soff[q]);
+                if (ALIGNED) to_lds4(from, base);
+                else to_lds1(from, base + q * 256);
+            }
         }
     };
 
@@ -748,7 +779,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const uint16_t* dbase;
     const uint8_t *cbase, *sbase;
     uint32_t doff[4];
-    bool cin, sin;
+    bool cin, sin, whole;                                // columns of this lane's, of the whole tile
     const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ ((wave & 1) << 2), srow = wave * 8 + (lane & 7);
     const uint32_t coff = crow * (uint32_t)(p.K / 2) + cunit * 16, soff = srow * (uint32_t)KB + (lane >> 3);
     const int du = (lane & 7) ^ (lane >> 3);
@@ -758,26 +789,36 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
         sbase = p.w_s + (int64_t)n.g * p.N * KB + n.nt * 8;
         cin = n.nt * 8 + cunit < KB;
         sin = n.nt * 8 + (lane >> 3) < KB;
+        whole = n.nt * 8 + 8 <= KB;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int r = (wave * 4 + q) * 8 + (lane >> 3);
-            doff[q] = (uint32_t)(min(r, n.re - 1 - n.rb) * p.as + (du ^ (q & 1)) * 8);
+            doff[q] = (uint32_t)(min(r, n.re - 1 - n.rb) * p.as + (du ^ (q & 1)) * 8) * 2;
         }
     };
     auto issue = [&](int s, int slot) {
         uint8_t* base = smem + slot * kGSlot;
-        const uint16_t* db = scalar(dbase + s * 64);
+        const uint16_t* db = dbase + s * 64;
+        const uint8_t* cs = cbase + (int64_t)s * 64 * (p.K / 2);
+        const uint8_t* ss = sbase + (int64_t)s * 64 * KB;
+        uint8_t *cd = base + kGDout + wave * 1024, *sd = base + kGDout + kGCodes + wave * 256;
+        if (VECTOR && whole && s * 64 + 64 <= p.N) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint8_t* dst = base + (wave * 4 + q) * 1024;
-            const int left = p.N - s * 64 - (du ^ (q & 1)) * 8;
-            if (VECTOR) to_lds16(within(left > 0, db + doff[q]), dst);
-            else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16<false>(db + doff[q], left);
+            for (int q = 0; q < 4; ++q) load_lds<16>(db, doff[q], base + (wave * 4 + q) * 1024);
+            load_lds<16>(cs, coff, cd);
+            load_lds<1>(ss, soff, sd);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint8_t* dst = base + (wave * 4 + q) * 1024;
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(db) + doff[q]);
+                const int left = p.N - s * 64 - (du ^ (q & 1)) * 8;
+                if (VECTOR) to_lds16(within(left > 0, src), dst);
+                else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16<false>(src, left);
+            }
+            to_lds16(within(cin && s * 64 + crow < p.N, cs + coff), cd);
+            to_lds1(within(sin && s * 64 + srow < p.N, ss + soff), sd);
         }
-        to_lds16(within(cin && s * 64 + crow < p.N, scalar(cbase + (int64_t)s * 64 * (p.K / 2)) + coff),
-                 base + kGDout + wave * 1024);
-        to_lds1(within(sin && s * 64 + srow < p.N, scalar(sbase + (int64_t)s * 64 * KB) + soff),
-                base + kGDout + kGCodes + wave * 256);
     };
     int next = mine, is = 0;                             // tile and stage of the next loads
     bool more = true;
