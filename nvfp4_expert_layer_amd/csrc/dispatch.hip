@@ -7,7 +7,8 @@
 //   out_t     = sum_j w_tj rows[inv_tj]         drows[inv_tj] = w_tj dout_t
 //                                               dw_tj = dout_t . rows[inv_tj]
 // All of it moves bytes: a row element costs at most three operations, so every
-// kernel reads or writes 16 bytes a lane and each row once.  The gather runs by
+// kernel reads or writes 16 bytes a lane and each row once.  Rows need no alignment and
+// no particular width: a row's last unit ends with the row and overlaps the one before.  The gather runs by
 // token (a token's row is loaded once and stored to its k places), not by sorted
 // row (which would load it k times).
 #include "device_common.h"
@@ -20,8 +21,8 @@ constexpr int kChunk = 256;                    // pairs per block at most
 constexpr int kMaxExperts = 1024;
 
 // ---------------------------------------------------------------------------
-// Row elements: 16-byte vectors of VEC elements, or single elements (VEC 1) for
-// rows that are not 16-byte aligned.
+// Row elements: 16-byte units of VEC elements, or single elements (VEC 1) for rows
+// shorter than a unit.  Unit u of a row of d elements starts at unit_start.
 // ---------------------------------------------------------------------------
 template <int DT> struct Elem;
 template <> struct Elem<kBF16> { typedef uint16_t type; };
@@ -45,11 +46,13 @@ template <int DT, bool VECTOR>
 struct Row {
     typedef typename Elem<DT>::type E;
     static constexpr int VEC = VECTOR ? 16 / (int)sizeof(E) : 1;
+    static __host__ __device__ int units(int d) { return (d + VEC - 1) / VEC; }
+    static __device__ int unit_start(int u, int d) { return min(u * VEC, d - VEC); }
     struct Raw { uint32_t w[VECTOR ? 4 : 1]; };
     static __device__ __forceinline__ Raw load(const void* base, int64_t el) {
         Raw r;
         if constexpr (VECTOR) {
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const E*>(base) + el);
+            const u32x4_t v = *reinterpret_cast<const u32x4_any_t*>(static_cast<const E*>(base) + el);
             r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
         } else {
             r.w[0] = static_cast<const E*>(base)[el];
@@ -69,14 +72,14 @@ struct Row {
         } else if constexpr (sizeof(E) == 4) {
             __builtin_nontemporal_store(u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                                                 __float_as_uint(f[3])},
-                                        reinterpret_cast<u32x4_t*>(p));
+                                        reinterpret_cast<u32x4_any_t*>(p));
         } else {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 o[i] = DT == kBF16 ? f32x2_to_bf16x2(f[2 * i], f[2 * i + 1])
                                    : from_f32<DT>(f[2 * i]) | (from_f32<DT>(f[2 * i + 1]) << 16);
-            __builtin_nontemporal_store(u32x4_t{o[0], o[1], o[2], o[3]}, reinterpret_cast<u32x4_t*>(p));
+            __builtin_nontemporal_store(u32x4_t{o[0], o[1], o[2], o[3]}, reinterpret_cast<u32x4_any_t*>(p));
         }
     }
 };
@@ -127,14 +130,15 @@ __device__ __forceinline__ int local_expert(const DispatchArgs& a, int p) {
 }
 
 // One block takes the pairs of tpb tokens (at most kChunk pairs): their places,
-// then their rows' copies in units of U bytes.  grid.y splits the columns.
+// then their rows' copies in units U (a row: `bytes` bytes; strides in bytes).  grid.y
+// splits the columns.
 //
 // COUNTED = false (one launch): the block counts all T k ids by itself, those
 // before its own pairs and the rest apart, in LDS; integer counts do not depend
 // on the order of the atomics.  COUNTED = true: the two kernels below have left
 // the counts per block in the workspace.
 template <typename U, bool COUNTED>
-__global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a, int tpb, int blocks, int units,
+__global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a, int tpb, int blocks, int units, int bytes,
                                                             int64_t xs, int64_t rs) {
     __shared__ int before[kMaxExperts], base[kMaxExperts], lid[kChunk], dest[kChunk], part[4];
     const int tid = threadIdx.x, L = a.L;
@@ -184,16 +188,16 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a, int 
     if (!a.x) return;
     __syncthreads();
 
-    const U* x = static_cast<const U*>(a.x);
-    U* rows = static_cast<U*>(a.rows);
+    const char* x = static_cast<const char*>(a.x);
+    char* rows = static_cast<char*>(a.rows);
     const int per = (units + gridDim.y - 1) / gridDim.y, u0 = blockIdx.y * per, nu = min(per, units - u0);
     if (nu <= 0) return;
     for (int i = tid; i < nt * nu; i += kThreads) {
-        const int t = i / nu, u = u0 + (i - t * nu);
-        const U v = x[(t0 + t) * xs + u];
+        const int t = i / nu, c = min((u0 + (i - t * nu)) * (int)sizeof(U), bytes - (int)sizeof(U));
+        const U v = *reinterpret_cast<const U*>(x + (t0 + t) * xs + c);
         for (int j = 0; j < a.k; ++j) {
             const int r = dest[t * a.k + j];
-            if (r >= 0) __builtin_nontemporal_store(v, &rows[r * rs + u]);
+            if (r >= 0) __builtin_nontemporal_store(v, reinterpret_cast<U*>(rows + r * rs + c));
         }
     }
 }
@@ -237,17 +241,17 @@ DispatchPlan dispatch_plan(int T, int k) {
     DispatchPlan p;
     p.one_launch = (int64_t)T * k <= kOneLaunchPairs;
     // one launch: one token a block until there are blocks enough to fill the card; else
-    // whole chunks, for each block leaves a count per expert
-    const int most = kChunk / k, few = T / 1024 < 1 ? 1 : T / 1024;
-    p.tokens_per_block = !p.one_launch || few > most ? most : few;
+    // a block a CU before blocks take whole chunks, for each leaves a count per expert
+    const int most = kChunk / k, few = T / (p.one_launch ? 1024 : 256);
+    p.tokens_per_block = few < 1 ? 1 : (few > most ? most : few);
     p.blocks = (T + p.tokens_per_block - 1) / p.tokens_per_block;
     return p;
 }
 
 template <typename U>
 static void dispatch_units(const DispatchArgs& a, const DispatchPlan& p, hipStream_t s) {
-    const int eb = dtype_bytes(a.dtype), per = (int)sizeof(U) / eb;
-    const int units = a.x ? a.d / per : 0;
+    const int eb = dtype_bytes(a.dtype), bytes = a.d * eb;
+    const int units = a.x ? (bytes + (int)sizeof(U) - 1) / (int)sizeof(U) : 0;
     // few blocks: the columns over several too, at least 64 units each
     const int want = p.one_launch ? 256 : 512, most = (units + 63) / 64;
     int split = want / p.blocks;
@@ -256,29 +260,21 @@ static void dispatch_units(const DispatchArgs& a, const DispatchPlan& p, hipStre
     const dim3 grid(p.blocks, split);
     if (p.one_launch) {
         hipLaunchKernelGGL((dispatch_kernel<U, false>), grid, dim3(kThreads), 0, s, a, p.tokens_per_block, p.blocks,
-                           units, a.xs / per, a.rs / per);
+                           units, bytes, a.xs * eb, a.rs * eb);
         return;
     }
     hipLaunchKernelGGL(dispatch_count_kernel, dim3(p.blocks), dim3(kThreads), 0, s, a, p.tokens_per_block, p.blocks);
     hipLaunchKernelGGL(dispatch_scan_kernel, dim3(a.L), dim3(kThreads), 0, s, a, p.blocks);
     hipLaunchKernelGGL((dispatch_kernel<U, true>), grid, dim3(kThreads), 0, s, a, p.tokens_per_block, p.blocks, units,
-                       a.xs / per, a.rs / per);
+                       bytes, a.xs * eb, a.rs * eb);
 }
 
 // Blocks of a grid-stride launch: a grid holds fewer than 2^32 threads.
 static unsigned grid_blocks(int64_t n) { return (unsigned)(n < (1 << 22) ? n : (1 << 22)); }
 
-static bool aligned16(const void* p, int64_t stride, int eb) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (stride * eb) % 16 == 0;
-}
-
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
     const DispatchPlan p = dispatch_plan(a.T, a.k);
-    const int eb = dtype_bytes(a.dtype);
-    if ((int64_t)a.d * eb % 16 == 0 && aligned16(a.x, a.xs, eb) && aligned16(a.rows, a.rs, eb))
-        dispatch_units<u32x4_t>(a, p, s);
-    else if (eb == 4) dispatch_units<uint32_t>(a, p, s);
-    else if (eb == 2) dispatch_units<uint16_t>(a, p, s);
+    if (a.d * dtype_bytes(a.dtype) >= 16) dispatch_units<u32x4_any_t>(a, p, s);
     else dispatch_units<uint8_t>(a, p, s);
     return hipGetLastError();
 }
@@ -293,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
     typedef Row<DT, VECTOR> R;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)a.T * units;
          i += (int64_t)gridDim.x * blockDim.x) {
-        const int t = (int)(i / units), c0 = (int)(i - (int64_t)t * units) * R::VEC, pairs = a.T * a.k;
+        const int t = (int)(i / units), c0 = R::unit_start((int)(i - (int64_t)t * units), a.d), pairs = a.T * a.k;
         float acc[R::VEC];
 #pragma unroll
         for (int e = 0; e < R::VEC; ++e) acc[e] = 0.f;
@@ -324,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
 
 template <int DT, bool VECTOR>
 static void combine_rows(const CombineRowsArgs& a, hipStream_t s) {
-    const int units = a.d / Row<DT, VECTOR>::VEC;
+    const int units = Row<DT, VECTOR>::units(a.d);
     const int64_t n = (int64_t)a.T * units;
     // few outputs: one wave a block, so that they spread over the CUs
     const int threads = n <= 64 * 256 ? 64 : kThreads;
@@ -336,8 +332,7 @@ static void combine_rows(const CombineRowsArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine_rows(const CombineRowsArgs& a, hipStream_t s) {
-    const int eb = dtype_bytes(a.dtype);
-    const bool v = (int64_t)a.d * eb % 16 == 0 && aligned16(a.rows, a.rs, eb) && aligned16(a.out, a.os, eb);
+    const bool v = a.d * dtype_bytes(a.dtype) >= 16;
     if (a.dtype == kBF16) v ? combine_rows<kBF16, true>(a, s) : combine_rows<kBF16, false>(a, s);
     else if (a.dtype == kF16) v ? combine_rows<kF16, true>(a, s) : combine_rows<kF16, false>(a, s);
     else v ? combine_rows<kF32, true>(a, s) : combine_rows<kF32, false>(a, s);
@@ -357,6 +352,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
     __shared__ float red[kThreads / 64][8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wt = wave % WAVES, pairs = a.T * a.k;
+    const bool tail = a.d % R::VEC != 0;                        // a row's last unit overlaps the one before
     // tokens TOKENS * gridDim.x apart; with four waves a token, a block's waves share t
     for (int64_t t = (int64_t)blockIdx.x * TOKENS + wave / WAVES; t < a.T; t += (int64_t)gridDim.x * TOKENS)
     for (int j0 = 0; j0 < a.k; j0 += 8) {
@@ -370,7 +366,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
             dot[q] = 0.f;
         }
         for (int u = wt * 64 + lane; u < units; u += 64 * WAVES) {
-            const int c0 = u * R::VEC;
+            const int c0 = R::unit_start(u, a.d), old = u * R::VEC - c0;   // elements of the unit before
             const typename R::Raw g = R::load(a.dout, t * a.dos + c0);
             typename R::Raw y[8];
             if (a.dw) {
@@ -387,9 +383,13 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
                     for (int e = 0; e < R::VEC; ++e) o[e] = w[q] * R::get(g, e);
                     R::store(a.drows, row[q] * a.drs + c0, o);
                 }
-                if (a.dw) {
+                if (a.dw && !tail) {
 #pragma unroll
                     for (int e = 0; e < R::VEC; ++e) dot[q] = fmaf(R::get(g, e), R::get(y[q], e), dot[q]);
+                } else if (a.dw) {
+#pragma unroll
+                    for (int e = 0; e < R::VEC; ++e)
+                        if (e >= old) dot[q] = fmaf(R::get(g, e), R::get(y[q], e), dot[q]);
                 }
             }
         }
@@ -419,7 +419,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
 
 template <int DT, bool VECTOR>
 static void combine_grad(const CombineGradArgs& a, hipStream_t s) {
-    const int units = a.d / Row<DT, VECTOR>::VEC;
+    const int units = Row<DT, VECTOR>::units(a.d);
     // a wave walks a narrow row alone; four share a wide one
     if (units <= 128)
         hipLaunchKernelGGL((combine_grad_kernel<DT, VECTOR, 1>), dim3(grid_blocks(((int64_t)a.T + 3) / 4)), dim3(kThreads), 0, s,
@@ -430,9 +430,7 @@ static void combine_grad(const CombineGradArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
-    const int eb = dtype_bytes(a.dtype);
-    const bool v = (int64_t)a.d * eb % 16 == 0 && aligned16(a.dout, a.dos, eb) &&
-                   (!a.dw || aligned16(a.rows, a.rs, eb)) && (!a.drows || aligned16(a.drows, a.drs, eb));
+    const bool v = a.d * dtype_bytes(a.dtype) >= 16;
     if (a.dtype == kBF16) v ? combine_grad<kBF16, true>(a, s) : combine_grad<kBF16, false>(a, s);
     else if (a.dtype == kF16) v ? combine_grad<kF16, true>(a, s) : combine_grad<kF16, false>(a, s);
     else v ? combine_grad<kF32, true>(a, s) : combine_grad<kF32, false>(a, s);

@@ -74,8 +74,8 @@ __device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[DT == kF32 ? 8 :
 }
 
 // Piece i: eight elements.  per_row pieces a row; FLAT: rows follow each other
-// without gaps (x is one long row).  VECTOR: 16-byte loads (aligned rows).
-template <int DT, bool FLAT, bool VECTOR>
+// without gaps (x is one long row).
+template <int DT, bool FLAT>
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void* __restrict__ x, int64_t pieces, int per_row,
                                                              int64_t xs, uint8_t* __restrict__ codes,
                                                              uint8_t* __restrict__ scales) {
@@ -89,20 +89,11 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void* __restr
             el = r * xs + (i - r * per_row) * 8;
         }
         uint32_t w[W];
-        if constexpr (VECTOR) {
-            const u32x4_t* src = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(x) + el * (W / 2));
+        const u32x4_any_t* src = reinterpret_cast<const u32x4_any_t*>(static_cast<const char*>(x) + el * (W / 2));
 #pragma unroll
-            for (int q = 0; q < W / 4; ++q) {
-                const u32x4_t v = src[q];
-                w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
-            }
-        } else if constexpr (DT == kF32) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = static_cast<const uint32_t*>(x)[el + q];
-        } else {
-            const uint16_t* src = static_cast<const uint16_t*>(x) + el;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = src[2 * q] | ((uint32_t)src[2 * q + 1] << 16);
+        for (int q = 0; q < W / 4; ++q) {
+            const u32x4_t v = src[q];
+            w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
         }
         const int field = (int)(quad_max(top_bits<DT>(w)) >> 23);
         const bool bad = field == 255;                     // Inf or NaN in the block
@@ -114,7 +105,7 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void* __restr
 }
 
 // Piece i: 16 bytes of output (eight 16-bit or four fp32 values), per_row pieces a row.
-template <int DT, bool FLAT, bool VECTOR>
+template <int DT, bool FLAT>
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t pieces,
                                                                int per_row, void* __restrict__ out, int64_t os) {
@@ -152,16 +143,8 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __
             }
         }
         // streaming stores of consecutive lanes' consecutive 16 bytes
-        if constexpr (VECTOR) {
-            __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]},
-                                        reinterpret_cast<u32x4_t*>(static_cast<char*>(out) + el * (16 / N)));
-        } else if constexpr (DT == kF32) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) static_cast<uint32_t*>(out)[el + q] = w[q];
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) static_cast<uint16_t*>(out)[el + q] = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
-        }
+        __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]},
+                                    reinterpret_cast<u32x4_any_t*>(static_cast<char*>(out) + el * (16 / N)));
     }
 }
 
@@ -176,14 +159,11 @@ template <int DT>
 static void quantize_dt(const void* x, int64_t R, int C, int64_t xs, uint8_t* codes, uint8_t* scales, hipStream_t s) {
     const int64_t pieces = R * (C / 8);
     const dim3 grid(piece_blocks(pieces));
-    const int eb = dtype_bytes(DT);
-    const bool v = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (R == 1 || xs * eb % 16 == 0);
     const bool flat = R == 1 || xs == C;
     auto run = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, pieces, C / 8, xs, codes, scales);
     };
-    if (v) flat ? run(mxfp4_quantize_kernel<DT, true, true>) : run(mxfp4_quantize_kernel<DT, false, true>);
-    else flat ? run(mxfp4_quantize_kernel<DT, true, false>) : run(mxfp4_quantize_kernel<DT, false, false>);
+    flat ? run(mxfp4_quantize_kernel<DT, true>) : run(mxfp4_quantize_kernel<DT, false>);
 }
 
 template <int DT>
@@ -192,14 +172,11 @@ static void dequantize_dt(const uint8_t* codes, const uint8_t* scales, int64_t R
     constexpr int n = DT == kF32 ? 4 : 8;
     const int64_t pieces = R * (C / n);
     const dim3 grid(piece_blocks(pieces));
-    const int eb = dtype_bytes(DT);
-    const bool v = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && (R == 1 || os * eb % 16 == 0);
     const bool flat = R == 1 || os == C;
     auto run = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, codes, scales, pieces, C / n, out, os);
     };
-    if (v) flat ? run(mxfp4_dequantize_kernel<DT, true, true>) : run(mxfp4_dequantize_kernel<DT, false, true>);
-    else flat ? run(mxfp4_dequantize_kernel<DT, true, false>) : run(mxfp4_dequantize_kernel<DT, false, false>);
+    flat ? run(mxfp4_dequantize_kernel<DT, true>) : run(mxfp4_dequantize_kernel<DT, false>);
 }
 
 hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t R, int C, int64_t xs, uint8_t* codes,

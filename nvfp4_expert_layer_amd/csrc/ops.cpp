@@ -147,7 +147,6 @@ moe::ProductArgs product_args(const moe_product_problem* p, const void* a, int64
     g.M = p->rows; g.N = p->n; g.K = p->k; g.G = p->groups;
     g.a = a; g.as = as; g.w = w; g.w_s = w_scales; g.offsets = offsets;
     g.out = out; g.out_dtype = out_dtype; g.os = os;
-    g.out_vec = !misaligned(out, (size_t)4 * moe::dtype_bytes(out_dtype)) && (p->rows <= 1 || os % 4 == 0) ? 1 : 0;
     return g;
 }
 

@@ -68,7 +68,6 @@ struct ProductArgs {
     void* out;                    // forward [M][N]; backward [M][K]
     int out_dtype;
     int64_t os;
-    int out_vec;                  // rows of out start at multiples of four elements' size
 };
 // cus: compute units of the device; a: the rows, or (backward) dout bf16 [M][N]
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s);

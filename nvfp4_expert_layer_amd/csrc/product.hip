@@ -107,7 +107,7 @@ __device__ __forceinline__ void stream_tiles(const ProductArgs& p, int g, int r0
         for (int w = 1; w < kSWaves; ++w) s += red[w * NR * NT * 64 + x];
         const int l = x & 63, t = (x >> 6) % NT, i = (x >> 6) / NT;
         const int r = r0 + 16 * t + (l & 15), n = n0 + 16 * i + 4 * (l >> 4);
-        if (r < re) store4(p.out, p.out_dtype, r * p.os + n, s, p.N - n, p.out_vec);
+        if (r < re) store4(p.out, p.out_dtype, r * p.os + n, s, p.N - n);
     }
 }
 
@@ -227,7 +227,7 @@ __device__ __forceinline__ void resident_tiles(const ProductArgs& p, int g, int 
 #pragma unroll
             for (int v = 1; v < kRWaves; ++v) sum += buf[(v * NT + i) * 64 + lane];
             const int r = r0 + 16 * i + col, n = t * 16 + 4 * lg;
-            if (r < re) store4(p.out, p.out_dtype, r * p.os + n, sum, p.N - n, p.out_vec);
+            if (r < re) store4(p.out, p.out_dtype, r * p.os + n, sum, p.N - n);
         }
     };
     Weight w0, w1;
@@ -311,7 +311,7 @@ hipError_t launch_product_stream(const ProductArgs& p, int cus, hipStream_t s) {
 // ---------------------------------------------------------------------------
 constexpr int kGWaves = 8;
 
-template <int NT, bool VECTOR>
+template <int NT>
 __device__ __forceinline__ void grad_tiles(const ProductArgs& p, int g, int r0, int re, int k0, float* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
     const int KB = p.K / 32, kc = k0 + 8 * col;                 // this lane's columns kc .. kc + 7
@@ -341,7 +341,7 @@ __device__ __forceinline__ void grad_tiles(const ProductArgs& p, int g, int r0, 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + col;
-            st.dv[t] = r < re ? load8_bf16<VECTOR>(dout + r * p.as + n, p.N - n) : u32x4_t{0u, 0u, 0u, 0u};
+            st.dv[t] = r < re ? load8_bf16(dout + r * p.as + n, p.N - n) : u32x4_t{0u, 0u, 0u, 0u};
         }
     };
     auto multiply = [&](int ns, Step& st) {
@@ -387,11 +387,10 @@ __device__ __forceinline__ void grad_tiles(const ProductArgs& p, int g, int r0, 
             for (int w = 1; w < kGWaves; ++w) f[c] += red[((w * 4 + v) * 8 + 4 * q + c) * 64 + l];
         }
         const int r = r0 + 16 * t + (l & 15), k = k0 + 8 * (4 * (l >> 4) + v) + 4 * q;
-        if (r < re && k < p.K) store4(p.out, p.out_dtype, r * p.os + k, f, 4, p.out_vec);
+        if (r < re && k < p.K) store4(p.out, p.out_dtype, r * p.os + k, f, 4);
     }
 }
 
-template <bool VECTOR>
 __global__ __launch_bounds__(64 * kGWaves) void product_grad_stream_kernel(ProductArgs p, int by_rank) {
     __shared__ float red[kGWaves * 32 * 64];
     const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
@@ -400,8 +399,8 @@ __global__ __launch_bounds__(64 * kGWaves) void product_grad_stream_kernel(Produ
     group_rows(p, g, rb, re);
     const int k0 = blockIdx.x * 128;
     for (int r0 = rb; r0 < re;) {
-        if (re - r0 > 16) { grad_tiles<2, VECTOR>(p, g, r0, re, k0, red); r0 += 32; }
-        else { grad_tiles<1, VECTOR>(p, g, r0, re, k0, red); r0 += 16; }
+        if (re - r0 > 16) { grad_tiles<2>(p, g, r0, re, k0, red); r0 += 32; }
+        else { grad_tiles<1>(p, g, r0, re, k0, red); r0 += 16; }
     }
 }
 
@@ -409,10 +408,7 @@ hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
     const int groups = min(p.G, p.M);
     const dim3 grid((p.K + 127) / 128, groups);
     const int by_rank = p.M < p.G ? 1 : 0;
-    if (dout_vector(p))
-        hipLaunchKernelGGL((product_grad_stream_kernel<true>), grid, dim3(64 * kGWaves), 0, s, p, by_rank);
-    else
-        hipLaunchKernelGGL((product_grad_stream_kernel<false>), grid, dim3(64 * kGWaves), 0, s, p, by_rank);
+    hipLaunchKernelGGL(product_grad_stream_kernel, grid, dim3(64 * kGWaves), 0, s, p, by_rank);
     return hipGetLastError();
 }
 

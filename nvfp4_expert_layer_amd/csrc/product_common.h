@@ -76,28 +76,28 @@ __device__ __forceinline__ f32x4_t mfma_bf16_16(const u32x4_t& a, const u32x4_t&
                                                    c, 0, 0, 0);
 }
 
-// Eight bf16 from p, of which `left` exist (the others 0).  VECTOR: p is 16-byte
-// aligned and left is <= 0 or >= 8.
-template <bool VECTOR>
+// Eight bf16 from p (at any element), of which `left` exist (the others 0).
 __device__ __forceinline__ u32x4_t load8_bf16(const uint16_t* p, int left) {
+    if (left >= 8) return *reinterpret_cast<const u32x4_any_t*>(p);
     u32x4_t v = {0u, 0u, 0u, 0u};
-    if constexpr (VECTOR) {
-        if (left > 0) v = *reinterpret_cast<const u32x4_t*>(p);
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    }
+    for (int i = 0; i < 8; ++i)
+        if (i < left) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
     return v;
 }
 
+// Four outputs to two dwords of bf16 or f16.
+__device__ __forceinline__ u32x2_t pack4(int dtype, float a, float b, float c, float d) {
+    if (dtype == kBF16) return u32x2_t{f32x2_to_bf16x2(a, b), f32x2_to_bf16x2(c, d)};
+    return u32x2_t{f32_to_f16_bits(a) | (f32_to_f16_bits(b) << 16), f32_to_f16_bits(c) | (f32_to_f16_bits(d) << 16)};
+}
+
 // Four consecutive outputs of a row, of which `left` exist, at element `el`.
-// vec: groups of four start at 8-byte (f32: 16-byte) boundaries.
-__device__ __forceinline__ void store4(void* out, int dtype, int64_t el, const f32x4_t& f, int left, int vec) {
+__device__ __forceinline__ void store4(void* out, int dtype, int64_t el, const f32x4_t& f, int left) {
     if (dtype == kF32) {
         float* o = static_cast<float*>(out) + el;
-        if (vec && left >= 4) {
-            *reinterpret_cast<f32x4_t*>(o) = f;
+        if (left >= 4) {
+            *reinterpret_cast<u32x4_any_t*>(o) = __builtin_bit_cast(u32x4_t, f);
             return;
         }
 #pragma unroll
@@ -105,26 +105,18 @@ __device__ __forceinline__ void store4(void* out, int dtype, int64_t el, const f
             if (i < left) o[i] = f[i];
         return;
     }
-    uint32_t lo, hi;
-    if (dtype == kBF16) {
-        lo = f32x2_to_bf16x2(f[0], f[1]);
-        hi = f32x2_to_bf16x2(f[2], f[3]);
-    } else {
-        lo = f32_to_f16_bits(f[0]) | (f32_to_f16_bits(f[1]) << 16);
-        hi = f32_to_f16_bits(f[2]) | (f32_to_f16_bits(f[3]) << 16);
-    }
+    const u32x2_t v = pack4(dtype, f[0], f[1], f[2], f[3]);
     uint16_t* o = static_cast<uint16_t*>(out) + el;
-    if (vec && left >= 4) {
-        *reinterpret_cast<u32x2_t*>(o) = u32x2_t{lo, hi};
+    if (left >= 4) {
+        *reinterpret_cast<u32x2_any_t*>(o) = v;
         return;
     }
-    if (left > 0) o[0] = (uint16_t)lo;
-    if (left > 1) o[1] = (uint16_t)(lo >> 16);
-    if (left > 2) o[2] = (uint16_t)hi;
-    if (left > 3) o[3] = (uint16_t)(hi >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
 }
 
-// dout's rows can be read in 16-byte pieces that end with the row.
+// dout's rows lie in aligned 16-byte pieces that end with the row (direct loads to LDS).
 inline bool dout_vector(const ProductArgs& p) {
     return p.N % 8 == 0 && (p.M <= 1 || p.as % 8 == 0) && (reinterpret_cast<uintptr_t>(p.a) & 15) == 0;
 }

@@ -161,13 +161,10 @@ __device__ __forceinline__ void stage4(const ProductArgs& p, uint8_t* smem, cons
     if (p.out_dtype == kF32) {
         if (t.rb + row < t.re)
             store4(p.out, kF32, (t.rb + row) * p.os + t.nt * kTN + col, f32x4_t{a, b, c, d},
-                   width - t.nt * kTN - col, p.out_vec);
+                   width - t.nt * kTN - col);
         return;
     }
-    u32x2_t v;
-    if (p.out_dtype == kBF16) v = u32x2_t{f32x2_to_bf16x2(a, b), f32x2_to_bf16x2(c, d)};
-    else v = u32x2_t{f32_to_f16_bits(a) | (f32_to_f16_bits(b) << 16), f32_to_f16_bits(c) | (f32_to_f16_bits(d) << 16)};
-    *reinterpret_cast<u32x2_t*>(smem + (row * kYS + col) * 2) = v;
+    *reinterpret_cast<u32x2_t*>(smem + (row * kYS + col) * 2) = pack4(p.out_dtype, a, b, c, d);
 }
 
 __device__ __forceinline__ void store_staged(const ProductArgs& p, const uint8_t* smem, const Tile& t, int width) {
@@ -175,13 +172,12 @@ __device__ __forceinline__ void store_staged(const ProductArgs& p, const uint8_t
     __syncthreads();
     const int nrow = t.re - t.rb, ncol = min(kTN, width - t.nt * kTN);
     uint16_t* out = static_cast<uint16_t*>(p.out) + t.rb * p.os + t.nt * kTN;
-    const bool vec = p.os % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
     for (int x = threadIdx.x; x < kTM * (kTN / 8); x += kTThreads) {
         const int row = x >> 5, c = (x & 31) * 8;
         if (row >= nrow) break;                          // rows grow with x
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + (row * kYS + c) * 2);
-        if (vec && c + 8 <= ncol) {
-            *reinterpret_cast<u32x4_t*>(out + row * p.os + c) = v;
+        if (c + 8 <= ncol) {
+            *reinterpret_cast<u32x4_any_t*>(out + row * p.os + c) = v;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -268,7 +264,7 @@ __device__ __forceinline__ Tile table_tile(const ProductArgs& p, const int* tabl
 // % 2) .. + 4 (the backward's column pairs).
 template <bool PAIRED>
 __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage, const Tile& t, int row0, int col0,
-                                           int width, const f32x16_t& acc, bool vec) {
+                                           int width, const f32x16_t& acc) {
     const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
     const int left = width - t.nt * kTN - col0;
     if (p.out_dtype == kF32) {
@@ -277,19 +273,14 @@ __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage,
             for (int g = 0; g < 4; ++g) {
                 const int c = PAIRED ? 16 * (g >> 1) + 8 * h + 4 * (g & 1) : 8 * g + 4 * h;
                 store4(p.out, kF32, (t.rb + row0 + r32) * p.os + t.nt * kTN + col0 + c,
-                       f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}, left - c, p.out_vec);
+                       f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}, left - c);
             }
         }
         return;
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        u32x2_t v;
-        if (p.out_dtype == kBF16)
-            v = u32x2_t{f32x2_to_bf16x2(acc[4 * g], acc[4 * g + 1]), f32x2_to_bf16x2(acc[4 * g + 2], acc[4 * g + 3])};
-        else
-            v = u32x2_t{f32_to_f16_bits(acc[4 * g]) | (f32_to_f16_bits(acc[4 * g + 1]) << 16),
-                        f32_to_f16_bits(acc[4 * g + 2]) | (f32_to_f16_bits(acc[4 * g + 3]) << 16)};
+        const u32x2_t v = pack4(p.out_dtype, acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
         const int unit = PAIRED ? 2 * (g >> 1) + h : g, half = PAIRED ? g & 1 : h;
         const uint32_t at = lds_offset(stage) + r32 * 64 + ((unit ^ (r32 >> 2)) & 3) * 16 + half * 8;
         // written out: before an ordinary LDS store the compiler waits for every direct
@@ -302,8 +293,8 @@ __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage,
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stage + r * 64 + ((u ^ (r >> 2)) & 3) * 16);
         if (t.rb + row0 + r >= t.re) continue;
         uint16_t* o = static_cast<uint16_t*>(p.out) + (t.rb + row0 + r) * p.os + t.nt * kTN + col0 + 8 * u;
-        if (vec && 8 * u + 8 <= left) {
-            *reinterpret_cast<u32x4_t*>(o) = v;
+        if (8 * u + 8 <= left) {
+            *reinterpret_cast<u32x4_any_t*>(o) = v;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -322,7 +313,6 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int wm = wave >> 2, wn = wave & 3;             // rows 128 wm .. +128, outputs 64 wn .. +64
     const int NT = (p.N + kTN - 1) / kTN, KB = p.K / 32, nc = (KB + 7) / 8, r32 = lane & 31;
-    const bool vec = p.os % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 
     // This workgroup's tiles: workgroup b runs on XCD b % 8, each XCD takes a contiguous
     // range (it shares the tile's rows and the group's weight in its L2), its workgroups
@@ -517,7 +507,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
             if (i >= nvi) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                wave_store<false>(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i], vec);
+                wave_store<false>(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i]);
         }
         mine += stride;
         if (!ALIGNED || mine >= end) break;
@@ -762,7 +752,6 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int r32 = lane & 31, wt = wave >> 2, wk = wave & 3;    // rows 128 wt .. +128, columns 64 wk .. +64
     const int NT = (p.K + kTN - 1) / kTN, KB = p.K / 32, nn = (p.N + 63) / 64;
-    const bool vec = p.os % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
     int* table = reinterpret_cast<int*>(smem + kGOffTable);
     const int all = tile_table(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
     const int end = min(((int)blockIdx.x & 7) * per + per, all);
@@ -814,7 +803,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
                 const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(db) + doff[q]);
                 const int left = p.N - s * 64 - (du ^ (q & 1)) * 8;
                 if (VECTOR) to_lds16(within(left > 0, src), dst);
-                else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16<false>(src, left);
+                else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16(src, left);
             }
             to_lds16(within(cin && s * 64 + crow < p.N, cs + coff), cd);
             to_lds1(within(sin && s * 64 + srow < p.N, ss + soff), sd);
@@ -944,7 +933,7 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
                     o[2 * v] = acc[0][i][8 * b + v];
                     o[2 * v + 1] = acc[1][i][8 * b + v];
                 }
-                wave_store<true>(p, stage, t, wt * 128 + i * 32, wk * 64 + b * 32, p.K, o, vec);
+                wave_store<true>(p, stage, t, wt * 128 + i * 32, wk * 64 + b * 32, p.K, o);
             }
         }
         mine += stride;
