@@ -193,12 +193,18 @@ __device__ __forceinline__ void store_staged(const ProductArgs& p, const uint8_t
 // are not aligned to dwords) each byte in a dword of its own, [blocks][256 rows].
 constexpr int scale_bytes(bool aligned, int blocks) { return 256 * blocks * (aligned ? 1 : 4); }
 constexpr int kMxCodes = 256 * 128;                         // an operand's 256 k of a stage
-constexpr int mx_slot(bool aligned) { return 2 * kMxCodes + 2 * scale_bytes(aligned, 8); }   // weight | rows; scales
+// weight | rows; with them the stage's scales, or (aligned) those of two stages apart, for
+// a row's few bytes cost a line access however many they are
+constexpr int mx_slot(bool aligned) { return 2 * kMxCodes + (aligned ? 0 : 2 * scale_bytes(false, 8)); }
+constexpr int kMxPair = 2 * scale_bytes(true, 16);          // two stages' scales of both operands
 constexpr int kWaveStage = 2048;                            // a wave's 32 x 32 outputs on their way out
 constexpr int kTable = (1024 + 1) * 4;
-// LDS: stages [2] | waves' staging [8] | table.  Without aligned scales the stages take
-// all 160 KB: one tile a workgroup, staged and looked up in the stages' place.
-constexpr int mx_lds(bool aligned) { return 2 * mx_slot(aligned) + (aligned ? kTWaves * kWaveStage + kTable : 0); }
+// LDS: stages [2] | scales [2] | waves' staging [8] (half a block each) | table.  Without
+// aligned scales the stages take all 160 KB: one tile a workgroup, staged and looked up in
+// the stages' place.
+constexpr int kMxOffS = 2 * mx_slot(true), kMxOffStage = kMxOffS + 2 * kMxPair;
+constexpr int kMxOffTable = kMxOffStage + kTWaves * kWaveStage / 2;
+constexpr int mx_lds(bool aligned) { return aligned ? kMxOffTable + kTable : 2 * mx_slot(false); }
 
 template <int OPSEL>
 __device__ __forceinline__ f32x16_t mfma_mx32(const u32x4_t& a, uint32_t as, const u32x4_t& b, uint32_t bs,
@@ -238,7 +244,8 @@ __device__ __forceinline__ int tile_table(const ProductArgs& p, int* table) {
     if (2 * tid + 1 <= p.G) table[2 * tid + 1] = at + n[0];
     if (tid == 0 && p.G == 1024) table[1024] = total;
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(total);
+    // (offsets that decrease could claim more tiles than the rows hold)
+    return __builtin_amdgcn_readfirstlane(min(total, p.M / kTM + p.G));
 }
 
 // Tile `logical` (tile-major, NT column blocks a tile) by search in the table.
@@ -303,12 +310,44 @@ __device__ __forceinline__ void wave_store(const ProductArgs& p, uint8_t* stage,
     }
 }
 
+// An accumulator through 1 KB, 16 outputs (tokens' 32-byte rows) at a time.
+__device__ __forceinline__ void wave_store_halves(const ProductArgs& p, uint8_t* stage, const Tile& t, int row0,
+                                                  int col0, int width, const f32x16_t& acc) {
+    const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
+    const int left = width - t.nt * kTN - col0;
+    if (p.out_dtype == kF32) {
+        wave_store<false>(p, stage, t, row0, col0, width, acc);
+        return;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int v0 = 8 * x + 4 * g;
+            const u32x2_t v = pack4(p.out_dtype, acc[v0], acc[v0 + 1], acc[v0 + 2], acc[v0 + 3]);
+            const uint32_t at = lds_offset(stage) + r32 * 32 + ((g ^ (r32 >> 3)) & 1) * 16 + h * 8;
+            asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(v) : "memory");
+        }
+        const int r = lane >> 1, u = lane & 1, c = 16 * x + 8 * u;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stage + r * 32 + ((u ^ (r >> 3)) & 1) * 16);
+        if (t.rb + row0 + r >= t.re) continue;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (t.rb + row0 + r) * p.os + t.nt * kTN + col0 + c;
+        if (c + 8 <= left) {
+            *reinterpret_cast<u32x4_any_t*>(o) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < left) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
 // A workgroup takes tiles one after another: while a tile's last stages are multiplied
 // the next tile's first ones are loaded, and its outputs leave while those land.
 // ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales).
 template <bool ALIGNED>
 __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
-    constexpr int kScales = scale_bytes(ALIGNED, 8), kSlot = mx_slot(ALIGNED);
+    constexpr int kScales = scale_bytes(ALIGNED, ALIGNED ? 16 : 8), kSlot = mx_slot(ALIGNED);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int wm = wave >> 2, wn = wave & 3;             // rows 128 wm .. +128, outputs 64 wn .. +64
@@ -317,7 +356,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     // This workgroup's tiles: workgroup b runs on XCD b % 8, each XCD takes a contiguous
     // range (it shares the tile's rows and the group's weight in its L2), its workgroups
     // tiles next to each other.
-    int* table = reinterpret_cast<int*>(smem + (ALIGNED ? 2 * kSlot + kTWaves * kWaveStage : 0));
+    int* table = reinterpret_cast<int*>(smem + (ALIGNED ? kMxOffTable : 0));
     const int all = tile_table(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
     const int end = min(((int)blockIdx.x & 7) * per + per, all);
     int mine = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
@@ -332,9 +371,10 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     // weight's rows 64 w .. +64, waves 4-7 the rows'.  Rows and outputs past the tile's
     // end: any valid row (their results are not stored).
     const uint8_t *wbase, *abase, *sbase;
-    uint32_t coff[4], aoff[4], soff[2];
+    uint32_t coff[4], aoff[4], soff[ALIGNED ? 4 : 1];
     const int cu = (lane & 7) ^ (lane >> 3), srow = (wave & 3) * 64;
-    const int sdst = 2 * kMxCodes + (wave < 4 ? 0 : kScales);
+    const int sdst = (ALIGNED ? kMxOffS : 2 * kMxCodes) + (wave < 4 ? 0 : kScales);
+    constexpr int kSLoads = ALIGNED ? 4 : 1;             // loads of 16 rows x four dwords, or (bytes) of 64 rows
     auto load_from = [&](const Tile& n) {
         const int n0 = n.nt * kTN;
         const int64_t w0 = (int64_t)n.g * p.N + n0;
@@ -349,12 +389,14 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
             aoff[q] = min(r, amax) * (uint32_t)(p.K / 2) + u * 16;
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int r = srow + (ALIGNED ? q * 32 + (lane >> 1) : lane);
-            soff[q] = min(r, wave < 4 ? wmax : amax) * (uint32_t)KB + (ALIGNED ? (lane & 1) * 4 : 0);
+        for (int q = 0; q < kSLoads; ++q) {
+            const int r = srow + (ALIGNED ? q * 16 + (lane >> 2) : lane);
+            soff[q] = min(r, wave < 4 ? wmax : amax) * (uint32_t)KB + (ALIGNED ? (lane & 3) * 4 : 0);
         }
     };
-    // part 0 .. 3: the wave's codes of both operands; 4: its scales
+    // part 0 .. 3: the wave's codes of both operands; 4: its scales (ALIGNED: at even stages
+    // this one's and the next's)
+    int spair = 0;                                       // their slot
     auto issue = [&](int c, int slot, int part) {
         uint8_t* base = smem + slot * kSlot;
         const bool whole = c * 8 + 8 <= KB;
@@ -372,12 +414,14 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
         } else {
             const uint8_t* sb = sbase + (int64_t)c * 8;
             if (ALIGNED) {
+                if (c & 1) return;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint8_t* sd = base + sdst + srow * 8 + q * 256;
-                    if (whole) load_lds<4>(sb, soff[q], sd);
-                    else to_lds4(within(c * 8 + (lane & 1) * 4 < KB, sb + soff[q]), sd);
+                for (int q = 0; q < 4; ++q) {
+                    uint8_t* sd = smem + spair * kMxPair + sdst + srow * 16 + q * 256;
+                    if (c * 8 + 16 <= KB) load_lds<4>(sb, soff[q], sd);
+                    else to_lds4(within(c * 8 + (lane & 3) * 4 < KB, sb + soff[q]), sd);
                 }
+                spair ^= 1;
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -413,14 +457,16 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
             av[f][i] = *reinterpret_cast<const u32x4_t*>(S + kMxCodes + swz8(wm * 128 + i * 32 + r32, 4 * h + m));
     };
     auto row_scales = [&](const uint8_t* S, int r) {     // blocks 4 h .. 4 h + 3 of row r
-        if (ALIGNED) return *reinterpret_cast<const uint32_t*>(S + r * 8 + 4 * h);
+        if (ALIGNED) return *reinterpret_cast<const uint32_t*>(S + r * 16 + 4 * h);
         uint32_t v = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v |= *reinterpret_cast<const uint32_t*>(S + (4 * h + i) * 1024 + r * 4) << (8 * i);
         return v;
     };
-    auto scales = [&](int slot) {
-        const uint8_t* S = smem + slot * kSlot + 2 * kMxCodes;
+    int rpair = 1;                                       // slot of the scales being read
+    auto scales = [&](int slot, int c) {                 // of stage c of its tile
+        if (!(c & 1)) rpair ^= 1;
+        const uint8_t* S = ALIGNED ? smem + kMxOffS + rpair * kMxPair + (c & 1) * 8 : smem + slot * kSlot + 2 * kMxCodes;
 #pragma unroll
         for (int j = 0; j < 2; ++j) wsn[j] = row_scales(S, wn * 64 + j * 32 + r32);
 #pragma unroll
@@ -460,7 +506,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
             group(std::integral_constant<int, 2>{});
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             operands(slot ^ 1, std::integral_constant<int, 0>{});
-            scales(slot ^ 1);
+            scales(slot ^ 1, c + 1 < nc ? c + 1 : 0);
             keep_order();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -488,7 +534,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     operands(0, std::integral_constant<int, 0>{});
-    scales(0);
+    scales(0, 0);
     take_scales();
     for (;;) {
 #pragma unroll
@@ -501,13 +547,13 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
         const int nvi = cols ? max(0, min(4, (t.re - t.rb - wm * 128 + 31) >> 5)) : 0;   // 32-row blocks with rows
         stages(nvi);
         if (!ALIGNED) __syncthreads();                   // staged in the stages' place
-        uint8_t* stage = smem + (ALIGNED ? 2 * kSlot : 0) + wave * kWaveStage;
+        uint8_t* stage = smem + (ALIGNED ? kMxOffStage : 0) + wave * kWaveStage / 2;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= nvi) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                wave_store<false>(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i]);
+                wave_store_halves(p, stage, t, wm * 128 + i * 32, wn * 64 + j * 32, p.N, acc[j][i]);
         }
         mine += stride;
         if (!ALIGNED || mine >= end) break;
