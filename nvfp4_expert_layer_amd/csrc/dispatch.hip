@@ -8,9 +8,13 @@
 //                                               dw_tj = dout_t . rows[inv_tj]
 // All of it moves bytes: a row element costs at most three operations, so every
 // kernel reads or writes 16 bytes a lane and each row once.  Rows need no alignment and
-// no particular width: a row's last unit ends with the row and overlaps the one before.  The gather runs by
-// token (a token's row is loaded once and stored to its k places), not by sorted
-// row (which would load it k times).
+// no particular width: a row's last unit ends with the row and overlaps the one before.
+// The gather runs by token (a token's row is loaded once and stored to its k places),
+// not by sorted row (which would load it k times).
+//
+// T=8192, k=8, d=4096 bf16, 320 experts (65536 rows, 537 MB): dispatch 116 us (5.2 TB/s of
+// rows read and written; a large copy reaches 4.95), its gradient and the combine 109
+// us, the combine's gradient 232 us (4.9 TB/s).  T=64: 5.0 us and 3.5 us of kernel.
 #include "device_common.h"
 #include "ops.h"
 
@@ -234,7 +238,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_scan_kernel(DispatchArgs a,
     if (threadIdx.x == 0) a.totals[blockIdx.x] = sum;
 }
 
-// Up to this many pairs each block counts them all by itself.
+// Up to this many pairs each block counts them all by itself.  One launch against three:
+// T=1024, k=4, d=512 7 against 20 us; T=2048, k=8 (the bound) 17 against 20 us at d=512,
+// 39 against 36 us at d=4096.
 constexpr int kOneLaunchPairs = 16384;
 
 DispatchPlan dispatch_plan(int T, int k) {

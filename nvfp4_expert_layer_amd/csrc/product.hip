@@ -1,15 +1,24 @@
 // MXFP4 products over rows sorted by group, few rows a group (gfx950):
 //   forward   out[r][n]   = sum_k a[r][k] w[g(r)][n][k]
 //   backward  drows[r][k] = sum_n dout[r][n] w[g(r)][n][k]
-// Each group's weight is read once from memory per 64 (backward: 32) of its rows,
-// straight into registers in matrix-core operand order; a workgroup's waves split
-// the reduction and join their sums in LDS in wave order, so nothing depends on
-// timing.  With few rows the weight's bytes are the whole cost.
+// With few rows the weight's bytes are the whole cost: each group's weight is read once
+// from memory per 16 to 64 of its rows, straight into registers in matrix-core operand
+// order; a workgroup's waves split the reduction and join their sums in LDS in wave
+// order, so nothing depends on timing.
 //
-// Operand layouts (v_mfma_*_16x16x*): lane l holds row (or column) l % 16 and the
-// K slice of lane group l / 16; the accumulator's element v sits at row 4 (l/16) +
-// v, column l % 16.  The weight is the row operand, tokens are columns, so a lane
-// ends with four consecutive outputs of one token.
+//   product_resident_kernel  forward, K up to 4096 (W4A4: 8192).  512 rows over 160
+//       experts of 2048 x 4096: W4A16 136 us, 5.3 TB/s, W4A4 120 us, 6.0 TB/s (a large
+//       copy: 4.95); one row of 2048 x 4096: 4.9 us.  The form below it, which loads tokens
+//       again for each weight tile, took 216 us for the 512 rows.
+//   product_stream_kernel    forward, longer K.
+//   product_grad_stream_kernel  512 rows over 160 experts: 268 us, 2.7 TB/s; one row 8 us.
+//       Bound by its 4-byte loads (eight weight rows a lane) and their latency: without
+//       the next step's loads in flight 603 us.
+//
+// Operand layouts (v_mfma_*_16x16x*): lane l holds row (or column) l % 16 and the K
+// slice of lane group l / 16; the accumulator's element v sits at row 4 (l/16) + v,
+// column l % 16.  The weight is the row operand, tokens are columns, so a lane ends with
+// four consecutive outputs of one token.
 //   W4A4: v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 codes (16 bytes) and one E8M0
 //     scale a lane: one 32-element block as it lies in memory, no decoding.
 //   W4A16: 16 bytes of codes are four operands of v_mfma_f32_16x16x32_bf16;
@@ -262,9 +271,11 @@ __global__ __launch_bounds__(64 * kRWaves) void product_resident_kernel(ProductA
 
 template <bool MX, int KS, int MAXT>
 static void launch_resident(const ProductArgs& p, int cus, int groups, int by_rank, hipStream_t s) {
-    // tiles a workgroup: as many as leave four workgroups a CU
+    // tiles a workgroup: as many as leave one workgroup a CU, 16 at most. Experts of 2048 x
+    // 4096: 8 rows over 320 take 11.4 us, with two workgroups a CU 14.0; 512 rows over 160
+    // take 131 us, with at most 8 or 32 tiles 141 and 140.
     const int tiles = (p.N + 15) / 16;
-    const int per = max(1, min(16, (int)((int64_t)tiles * groups / (4 * cus))));
+    const int per = max(1, min(16, (int)((int64_t)tiles * groups / cus)));
     const dim3 grid((tiles + per - 1) / per, groups);
     // a wave's part of a scale row is one aligned load (per 16 bytes)
     constexpr int part = KS >= 4 ? 16 : 4 * KS;
@@ -282,19 +293,14 @@ template <bool MX>
 static hipError_t launch_stream(const ProductArgs& p, int cus, hipStream_t s) {
     const int groups = min(p.G, p.M);                           // at most so many hold rows
     const int by_rank = p.M < p.G ? 1 : 0;
-    // up to 8 rows a group on average: most groups fit 16 tokens, and the registers that
-    // 32 tokens would take keep more weights in flight
-    const bool one = p.M <= 8 * groups;
-#define RESIDENT(KS) \
-    (one ? launch_resident<MX, KS, 1>(p, cus, groups, by_rank, s) : launch_resident<MX, KS, 2>(p, cus, groups, by_rank, s))
-    if (p.K <= 1024) RESIDENT(1);
-    else if (p.K <= 2048) RESIDENT(2);
-    else if (p.K <= 4096) RESIDENT(4);
+    // (a variant for 16 tokens alone, with fewer registers, was no faster at any row count)
+    if (p.K <= 1024) launch_resident<MX, 1, 2>(p, cus, groups, by_rank, s);
+    else if (p.K <= 2048) launch_resident<MX, 2, 2>(p, cus, groups, by_rank, s);
+    else if (p.K <= 4096) launch_resident<MX, 4, 2>(p, cus, groups, by_rank, s);
     else if (MX && p.K <= 8192) launch_resident<true, 8, 1>(p, cus, groups, by_rank, s);
     else
         hipLaunchKernelGGL((product_stream_kernel<MX, 1>), dim3((p.N + 15) / 16, groups), dim3(64 * kSWaves), 0, s, p,
                            by_rank);
-#undef RESIDENT
     return hipGetLastError();
 }
 

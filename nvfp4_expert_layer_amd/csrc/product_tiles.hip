@@ -1,18 +1,35 @@
 // MXFP4 products in tiles, for many rows a group (gfx950).  A tile is 256 rows of
-// one group x 256 outputs; eight waves; the operands come through LDS rings filled
-// straight from global memory (global_load_lds), two or three stages ahead; one
-// workgroup a CU.  The weight is the matrix cores' row operand and tokens are their
-// columns, so that a lane ends with groups of four consecutive outputs of one token
-// (packed stores into the output's staging).
+// one group x 256 outputs; eight waves, one workgroup a CU (the operands' rings fill the
+// LDS); the operands come straight from global memory to LDS (global_load_lds).  The
+// weight is the matrix cores' row operand and tokens are their columns, so that a lane
+// ends with groups of four consecutive outputs of one token (packed stores).  An
+// operand is read from LDS one group of MFMAs ahead of its use, across the stage's
+// barrier too, so that the matrix cores do not wait for LDS.
 //
-//   mx_tile_kernel     W4A4: 32x32x64 scaled MFMAs on the codes as they lie in
-//                      memory; 128 k a stage, four stages.
-//   a16_tile_kernel    W4A16: bf16 rows, 64 k a stage, three stages; each wave
-//                      decodes its weight operand in registers (one conversion a
-//                      pair, the block scale within it), then 32x32x16 bf16 MFMAs.
-//   grad_tile_kernel   backward: the reduction runs over the weight's rows, 64 a
-//                      stage; a lane takes two neighbouring columns of eight rows,
-//                      decodes them and regroups the pairs by column.
+//   mx_tile_kernel     W4A4: 32x32x64 scaled MFMAs on the codes as they lie in memory;
+//                      256 k (a full line a row) a stage, two stages; a workgroup takes
+//                      tile after tile, the next one's stages loading while the last
+//                      one's outputs leave.  65536 rows over 320 experts of 2048 x 4096:
+//                      472 us, 2.33 PFLOP/s, 3.9 TB/s (its loads alone, without LDS reads
+//                      and MFMAs: 417 us); 16384 x 8192 x 8192: 638 us, 3.45 PFLOP/s (loads
+//                      alone 539 us).  Bound by the loads' line accesses and depth: 128 k a
+//                      stage in four stages (64-byte pieces) took 844 us, scales every stage
+//                      instead of every other 682 us, touching lines two stages early 716 us.
+//   a16_tile_kernel    W4A16: bf16 rows, 64 k a stage, three stages; each wave decodes
+//                      its weight operand in registers (one conversion a pair, the block
+//                      scale within it), then 32x32x16 bf16 MFMAs.  32768 rows over 64
+//                      experts of 2048 x 4096: 520 us, 1.06 PFLOP/s; 16384 x 8192 x 8192:
+//                      1.69 ms, 1.30 PFLOP/s, as a large bf16 product of the library (1.28).
+//                      The clock falls to 2.0 GHz under it; the matrix cores are busy 63% of
+//                      the cycles.
+//   grad_tile_kernel   backward: the reduction runs over the weight's rows, 64 a stage,
+//                      three stages; a lane takes two neighbouring columns of eight rows,
+//                      decodes them between the MFMAs and regroups the pairs by column.
+//                      32768 rows over 64 experts of 2048 x 4096: 620 us, 0.89 PFLOP/s;
+//                      16384 x 8192 x 8192: 1.93 ms, 1.14 PFLOP/s.  Timing-only variants of
+//                      the former: without the LDS reads 449 us, the loads 490, the decoding
+//                      554.  Four columns of a row half as wide (64 x 128 wave tiles): as
+//                      fast with 16-bit LDS reads, 677 us with eight rows' dwords side by side.
 //
 // Lane layout of the 32x32 MFMAs: lane l holds row (column) l % 32 and the K slice of
 // lane half l / 32; accumulator value v sits at row 8 (v/4) + 4 (l/32) + v % 4, column
