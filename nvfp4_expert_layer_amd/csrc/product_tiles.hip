@@ -48,19 +48,10 @@ namespace moe {
 constexpr int kTM = 256, kTN = 256, kTWaves = 8, kTThreads = 64 * kTWaves;
 
 typedef __attribute__((address_space(3))) void lds_void_t;
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
 
 static __device__ __align__(16) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
 
-__device__ __forceinline__ void to_lds16(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 16, 0, 0);
-}
-__device__ __forceinline__ void to_lds4(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 4, 0, 0);
-}
-// one byte a lane, each to a dword of its own
-__device__ __forceinline__ void to_lds1(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 1, 0, 0);
-}
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
 }
@@ -69,7 +60,8 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // (lane i at dst + i * max(BYTES, 4); dst is the same for the wave).  Written out: the
 // compiler adds 64-bit addresses a lane for each load inside a loop.  M0 holds the LDS
 // address (one wait state before its use); nothing comes back to registers, and the
-// kernels' own waits cover the loads.
+// kernels' own waits cover the loads (before a transposing LDS read the compiler waits
+// for every load of its own builtin).
 template <int BYTES>
 __device__ __forceinline__ void load_lds(const void* base, uint32_t off, const void* dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_offset(dst));
@@ -82,6 +74,20 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, const v
     else
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
                      ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
+}
+// The same from an address a lane.
+template <int BYTES>
+__device__ __forceinline__ void load_lds(const void* src, const void* dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_offset(dst));
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                     ::"v"(src), "s"(at) : "memory", "m0");
+    else if constexpr (BYTES == 4)
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+                     ::"v"(src), "s"(at) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off"
+                     ::"v"(src), "s"(at) : "memory", "m0");
 }
 // Operand reads stay before the MFMAs that follow them in the source (the scheduler
 // would sink each read to its use and wait for it there).
@@ -425,8 +431,8 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
                 load_lds<16>(ab, aoff[part], ad);
             } else {
                 const bool in = c * 8 + (cu ^ (part & 1)) < KB;
-                to_lds16(within(in, wb + coff[part]), wd);
-                to_lds16(within(in, ab + aoff[part]), ad);
+                load_lds<16>(within(in, wb + coff[part]), wd);
+                load_lds<16>(within(in, ab + aoff[part]), ad);
             }
         } else {
             const uint8_t* sb = sbase + (int64_t)c * 8;
@@ -436,7 +442,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
                 for (int q = 0; q < 4; ++q) {
                     uint8_t* sd = smem + spair * kMxPair + sdst + srow * 16 + q * 256;
                     if (c * 8 + 16 <= KB) load_lds<4>(sb, soff[q], sd);
-                    else to_lds4(within(c * 8 + (lane & 3) * 4 < KB, sb + soff[q]), sd);
+                    else load_lds<4>(within(c * 8 + (lane & 3) * 4 < KB, sb + soff[q]), sd);
                 }
                 spair ^= 1;
             } else {
@@ -444,7 +450,7 @@ __global__ __launch_bounds__(kTThreads) void mx_tile_kernel(ProductArgs p) {
                 for (int i = 0; i < 8; ++i) {
                     uint8_t* sd = base + sdst + i * 1024 + srow * 4;
                     if (whole) load_lds<1>(sb + i, soff[0], sd);
-                    else to_lds1(within(c * 8 + i < KB, sb + i + soff[0]), sd);
+                    else load_lds<1>(within(c * 8 + i < KB, sb + i + soff[0]), sd);
                 }
             }
         }
@@ -644,7 +650,7 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                to_lds16(within(ks * 8 + au[q] < KB * 4, reinterpret_cast<const uint8_t*>(ab) + aoff[q]),
+                load_lds<16>(within(ks * 8 + au[q] < KB * 4, reinterpret_cast<const uint8_t*>(ab) + aoff[q]),
                          base + q * 1024);
         }
     };
@@ -657,7 +663,7 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
         } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                to_lds16(within(c * 4 + cu[q] < KB, wb + coff[q]), base + (wave * 2 + q) * 1024);
+                load_lds<16>(within(c * 4 + cu[q] < KB, wb + coff[q]), base + (wave * 2 + q) * 1024);
         }
     };
     auto issue_scales = [&](int c, int slot) {            // c: of 256 k
@@ -670,8 +676,8 @@ __global__ __launch_bounds__(kTThreads) void a16_tile_kernel(ProductArgs p) {
                 load_lds<ALIGNED ? 4 : 1>(src, soff[q], base + q * 256);
             } else {
                 const void* from = within(c * 8 + sb < KB, src + soff[q]);
-                if (ALIGNED) to_lds4(from, base);
-                else to_lds1(from, base + q * 256);
+                if (ALIGNED) load_lds<4>(from, base);
+                else load_lds<1>(from, base + q * 256);
             }
         }
     };
@@ -824,17 +830,17 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 
     // ---- loads, three stages ahead ----
     // dout: four loads of 8 rows a wave and stage; codes: one of 8 weight rows x 128
-    // bytes, whose two 64-byte halves trade places in every other group of 8 rows (the
-    // two lane halves read rows 8 apart: different banks); scales: wave w's rows 8 w .. +8,
+    // bytes, unit u of a row in slot u ^ (row & 7) (a transposing read takes a unit of
+    // eight rows: different banks); scales: wave w's rows 8 w .. +8,
     // lane i block i / 8 of row i % 8, so that eight rows' scales of a block follow each
     // other.  Columns past K, rows past N: zeros.
     const uint16_t* dbase;
     const uint8_t *cbase, *sbase;
     uint32_t doff[4];
     bool cin, sin, whole;                                // columns of this lane's, of the whole tile
-    const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ ((wave & 1) << 2), srow = wave * 8 + (lane & 7);
+    const int crow = wave * 8 + (lane >> 3), cunit = (lane & 7) ^ (lane >> 3), srow = wave * 8 + (lane & 7);
     const uint32_t coff = crow * (uint32_t)(p.K / 2) + cunit * 16, soff = srow * (uint32_t)KB + (lane >> 3);
-    const int du = (lane & 7) ^ (lane >> 3);
+    const int du = cunit;
     auto load_from = [&](const Tile& n) {
         dbase = static_cast<const uint16_t*>(p.a) + (int64_t)n.rb * p.as;
         cbase = p.w + (int64_t)n.g * p.N * (p.K / 2) + n.nt * 128;
@@ -865,11 +871,11 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
                 uint8_t* dst = base + (wave * 4 + q) * 1024;
                 const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(db) + doff[q]);
                 const int left = p.N - s * 64 - (du ^ (q & 1)) * 8;
-                if (VECTOR) to_lds16(within(left > 0, src), dst);
+                if (VECTOR) load_lds<16>(within(left > 0, src), dst);
                 else *reinterpret_cast<u32x4_t*>(dst + lane * 16) = load8_bf16(src, left);
             }
-            to_lds16(within(cin && s * 64 + crow < p.N, cs + coff), cd);
-            to_lds1(within(sin && s * 64 + srow < p.N, ss + soff), sd);
+            load_lds<16>(within(cin && s * 64 + crow < p.N, cs + coff), cd);
+            load_lds<1>(within(sin && s * 64 + srow < p.N, ss + soff), sd);
         }
     };
     int next = mine, is = 0;                             // tile and stage of the next loads
@@ -884,34 +890,44 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
 
     // ---- the multiplication ----
     // Lane half h of substep q (16 n) takes weight rows 16 q + 8 h .. + 8 of the stage, two
-    // neighbouring columns of each: MFMA c's operand row i is column 2 i + c.  Substep q + 1
-    // is read from LDS before the MFMAs of substep q and decoded between them.
+    // neighbouring columns (a byte) of each: MFMA c's operand row i is column 2 i + c.  One
+    // transposing read brings the eight rows' bytes: 16 lanes read 8 rows x 16 bytes, lane i
+    // of them gets byte column i.  Substep q + 1 is read from LDS before the MFMAs of substep
+    // q and decoded between them.
     f32x16_t acc[2][4];
     u32x4_t op[2][2], dv[2][4];                          // operands by parity of the substep
-    uint32_t code[8];                                    // the next substep's codes and scales
+    i32x2_t code;                                        // the next substep's codes and scales
     u32x4_t sc[2];
+    const int erow = (lane & 15) >> 1;                   // of the eight rows, and where in it
+    const int coded = erow * 128 + (((2 * wk + ((lane >> 4) & 1)) ^ erow) << 4) + (lane & 1) * 8;
     auto read = [&](int sl, int q, auto f_c) {
         constexpr int f = decltype(f_c)::value;
         const uint8_t* D = smem + sl * kGSlot;
-        const uint8_t* C = D + kGDout + ((wk * 32) ^ (h * 64)) + r32 + (16 * q + 8 * h) * 128;
+        const uint8_t* C = D + kGDout + (16 * q + 8 * h) * 128 + coded;
         const uint8_t* S = D + kGDout + kGCodes + (2 * q + h) * 256 + (wk * 2 + (r32 >> 4)) * 32;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) code[j] = C[j * 128];
+        code = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t*)C);
 #pragma unroll
         for (int i = 0; i < 2; ++i) sc[i] = *reinterpret_cast<const u32x4_t*>(S + 16 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             dv[f][i] = *reinterpret_cast<const u32x4_t*>(D + swz8(wt * 128 + i * 32 + r32, 2 * q + h));
     };
-    auto decode = [&](int j, auto f_c) {                 // weight rows j and j + 1 of the eight
-        constexpr int f = decltype(f_c)::value;
+    auto decode = [&](auto j_c, auto f_c) {              // weight rows j and j + 1 of the eight
+        constexpr int j = decltype(j_c)::value, f = decltype(f_c)::value;
         const float s0 = __uint_as_float(sc[j / 4][j & 3] << 23);
         const float s1 = __uint_as_float(sc[j / 4][(j & 3) + 1] << 23);
-        const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[j], s0, 0));
-        const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[j + 1], s1, 0));
+        const uint32_t a =
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)code[j / 4], s0, j & 3));
+        const uint32_t b = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)code[j / 4], s1, (j & 3) + 1));
         op[f][0][j / 2] = __builtin_amdgcn_perm(b, a, 0x05040100u);
         op[f][1][j / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
     };
+    const std::integral_constant<int, 0> c0;
+    const std::integral_constant<int, 1> c1;
+    const std::integral_constant<int, 2> c2;
+    const std::integral_constant<int, 4> c4;
+    const std::integral_constant<int, 6> c6;
     // MFMAs of parity f, the other parity's decoding between them; FULL: four row blocks
     auto mfmas = [&](auto full_c, int nv, auto f_c, auto g_c) {
         constexpr bool FULL = decltype(full_c)::value;
@@ -923,13 +939,13 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
                 for (int c = 0; c < 2; ++c) acc[c][i] = mfma_bf16_32(op[f][c], dv[f][i], acc[c][i]);
             }
             keep_order();
-            if (i > 0) decode(2 * (i - 1), g_c);
-            if (i == 3) decode(6, g_c);
+            if (i == 1) decode(c0, g_c);
+            if (i == 2) decode(c2, g_c);
+            if (i == 3) decode(c4, g_c);
+            if (i == 3) decode(c6, g_c);
             keep_order();
         }
     };
-    const std::integral_constant<int, 0> c0;
-    const std::integral_constant<int, 1> c1;
     // The barrier stands before a stage's last MFMAs: its slot has been read (free for the
     // stage three on), and the wait has left only the last step's loads in flight.
     int slot = 0;
@@ -968,8 +984,10 @@ __global__ __launch_bounds__(kTThreads) void grad_tile_kernel(ProductArgs p) {
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     read(0, 0, c0);
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) decode(j, c0);
+    decode(c0, c0);
+    decode(c2, c0);
+    decode(c4, c0);
+    decode(c6, c0);
     for (;;) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
