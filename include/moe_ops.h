@@ -90,7 +90,7 @@ int moe_combine(const moe_dispatch_problem *p, const int32_t *inv, const float *
                 int64_t rows_stride, void *out, int64_t out_stride, void *stream);
 
 /* Gradients of moe_combine from dout [T][d] (the kept entries of inv distinct, as
- * moe_dispatch leaves them: a row that two pairs name holds either's gradient):
+ * moe_dispatch leaves them: what a row that two pairs name holds is not specified):
  *   drows    [T*k][d]  drows[inv[t][j]] = weights[t][j] * dout[t]; other rows are
  *                      left as they were (NULL to skip)
  *   dweights fp32 [T][k] = dout[t] . rows[inv[t][j]], 0 where not kept (NULL to

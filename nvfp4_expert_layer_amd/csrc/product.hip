@@ -7,7 +7,7 @@
 // order, so nothing depends on timing.
 //
 //   product_resident_kernel  forward, K up to 4096 (W4A4: 8192).  512 rows over 160
-//       experts of 2048 x 4096: W4A16 136 us, 5.3 TB/s, W4A4 120 us, 6.0 TB/s (a large
+//       experts of 2048 x 4096: W4A16 131 us, 5.4 TB/s, W4A4 122 us, 5.8 TB/s (a large
 //       copy: 4.95); one row of 2048 x 4096: 4.9 us.  The form below it, which loads tokens
 //       again for each weight tile, took 216 us for the 512 rows.
 //   product_stream_kernel    forward, longer K.

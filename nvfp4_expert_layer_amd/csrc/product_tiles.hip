@@ -15,21 +15,26 @@
 //                      alone 539 us).  Bound by the loads' line accesses and depth: 128 k a
 //                      stage in four stages (64-byte pieces) took 844 us, scales every stage
 //                      instead of every other 682 us, touching lines two stages early 716 us.
+//                      Groups' tiles of even height instead of 256 rows and a rest: within 1%.
 //   a16_tile_kernel    W4A16: bf16 rows, 64 k a stage, three stages; each wave decodes
 //                      its weight operand in registers (one conversion a pair, the block
 //                      scale within it), then 32x32x16 bf16 MFMAs.  32768 rows over 64
-//                      experts of 2048 x 4096: 520 us, 1.06 PFLOP/s; 16384 x 8192 x 8192:
-//                      1.69 ms, 1.30 PFLOP/s, as a large bf16 product of the library (1.28).
-//                      The clock falls to 2.0 GHz under it; the matrix cores are busy 63% of
-//                      the cycles.
+//                      experts of 2048 x 4096: 515 us, 1.07 PFLOP/s; 16384 x 8192 x 8192:
+//                      1.67 ms, 1.31 PFLOP/s, as a large bf16 product of the library (1.28).
+//                      The clock falls to 2.05 GHz under it; the matrix cores are busy half of
+//                      the former's cycles (a fifth of its tiles hold a few rows only).
 //   grad_tile_kernel   backward: the reduction runs over the weight's rows, 64 a stage,
-//                      three stages; a lane takes two neighbouring columns of eight rows,
-//                      decodes them between the MFMAs and regroups the pairs by column.
-//                      32768 rows over 64 experts of 2048 x 4096: 620 us, 0.89 PFLOP/s;
-//                      16384 x 8192 x 8192: 1.93 ms, 1.14 PFLOP/s.  Timing-only variants of
-//                      the former: without the LDS reads 449 us, the loads 490, the decoding
-//                      554.  Four columns of a row half as wide (64 x 128 wave tiles): as
-//                      fast with 16-bit LDS reads, 677 us with eight rows' dwords side by side.
+//                      three stages; a lane takes two neighbouring columns of eight rows
+//                      with one transposing LDS read, decodes them between the MFMAs and
+//                      regroups the pairs by column.  32768 rows over 64 experts of 2048 x
+//                      4096: 604 us, 0.91 PFLOP/s (617 with a read a row); 16384 x 8192 x
+//                      8192: 1.92 ms, 1.14 PFLOP/s.  No one resource bounds it: timing-only
+//                      variants of the former took 525 us without the row operands' LDS
+//                      reads, 523 without the decoding, 481 without the loads, and as long
+//                      without the scales' LDS reads.  64 x 128 wave tiles were as fast with
+//                      16-bit LDS reads and took 677 us with eight rows' dwords side by side;
+//                      four waves of 256 x 64 (half the decoding, one wave a SIMD) took 2.08 ms
+//                      on the latter product; tiles of even height 642 us on the former.
 //
 // Lane layout of the 32x32 MFMAs: lane l holds row (column) l % 32 and the K slice of
 // lane half l / 32; accumulator value v sits at row 8 (v/4) + 4 (l/32) + v % 4, column
