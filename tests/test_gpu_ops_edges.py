@@ -244,3 +244,64 @@ def test_one_workspace_under_two_graphs():
         for p, ids, b, g in graphs:
             c, o, pm, iv = dispatch.plan(ids.cpu().numpy(), p.local_expert_offset, p.num_local_experts)
             assert np.array_equal(b["inv"].cpu().numpy(), iv) and np.array_equal(b["offsets"].cpu().numpy(), o), r
+
+
+def _ragged(G, seed):
+    """Rows of G groups: empty ones, a few rows, tile edges and beyond; their offsets."""
+    gen = torch.Generator().manual_seed(seed)
+    pick = torch.tensor([0, 1, 31, 33, 128, 129, 255, 256, 257, 400, 512, 700])
+    counts = pick[torch.randint(0, len(pick), (G,), generator=gen)]
+    return torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+
+
+def _mx_values(codes, scales):
+    out = torch.empty(codes.shape[0], codes.shape[1] * 2, device="cuda")
+    return nv.moe_mxfp4_dequantize(codes, scales, out)
+
+
+@pytest.mark.parametrize("mode", ["w4a16", "w4a4"])
+@pytest.mark.parametrize("K", [32, 96, 128, 256, 288, 384, 512, 640])
+def test_tiles_one_after_another_of_few_stages(mode, K):
+    """About 1000 tiles, several a workgroup, of one to a few stages each.  Exact: with |a| <= 12,
+    |w| <= 12 products are multiples of 1/16 and sums of 640 below 2^17, so fp32 holds them."""
+    require_gpu()
+    log(f"{mode} many tiles K={K}")
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    G, N = 90, 1100
+    off = _ragged(G, K)
+    M = int(off[-1])
+    u8 = dict(dtype=torch.uint8, device="cuda", generator=gen)
+    w = nv.MXFP4Weights(torch.randint(0, 256, (G, N, K // 2), **u8), torch.randint(126, 129, (G, N, K // 32), **u8))
+    if mode == "w4a4":
+        a = nv.MXFP4Rows(torch.randint(0, 256, (M, K // 2), **u8), torch.randint(126, 129, (M, K // 32), **u8))
+        av = _mx_values(a.codes, a.scales)
+    else:
+        av = torch.randint(-8, 9, (M, K), generator=gen, device="cuda").float()
+        a = av.to(BF)
+    out = torch.full((M, N), 55.0, device="cuda")
+    nv.moe_mxfp4_product(nv.make_product_problem(M, N, K, G), a, w, off.int().cuda(), out)
+    for g in range(G):
+        b, e = int(off[g]), int(off[g + 1])
+        if e > b:
+            want = av[b:e] @ _mx_values(w.codes[g], w.scales[g]).t().contiguous()
+            assert torch.equal(out[b:e], want), (g, b, e)
+
+
+@pytest.mark.parametrize("N", [8, 13, 64, 72, 136, 200, 264])
+def test_gradient_tiles_one_after_another_of_few_stages(N):
+    """The same for the gradient (|dout| <= 8, |w| <= 12)."""
+    require_gpu()
+    log(f"gradient many tiles N={N}")
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    G, K = 90, 1120
+    off = _ragged(G, N)
+    M = int(off[-1])
+    u8 = dict(dtype=torch.uint8, device="cuda", generator=gen)
+    w = nv.MXFP4Weights(torch.randint(0, 256, (G, N, K // 2), **u8), torch.randint(126, 129, (G, N, K // 32), **u8))
+    dv = torch.randint(-8, 9, (M, N), generator=gen, device="cuda").float()
+    out = torch.full((M, K), 55.0, device="cuda")
+    nv.moe_mxfp4_product_backward(nv.make_product_problem(M, N, K, G), dv.to(BF), w, off.int().cuda(), out)
+    for g in range(G):
+        b, e = int(off[g]), int(off[g + 1])
+        if e > b:
+            assert torch.equal(out[b:e], dv[b:e] @ _mx_values(w.codes[g], w.scales[g])), (g, b, e)
