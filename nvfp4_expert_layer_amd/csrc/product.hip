@@ -11,9 +11,10 @@
 //       copy: 4.95); one row of 2048 x 4096: 4.9 us.  The form below it, which loads tokens
 //       again for each weight tile, took 216 us for the 512 rows.
 //   product_stream_kernel    forward, longer K.
-//   product_grad_stream_kernel  512 rows over 160 experts: 268 us, 2.7 TB/s; one row 8 us.
-//       Bound by its 4-byte loads (eight weight rows a lane) and their latency: without
-//       the next step's loads in flight 603 us.
+//   product_grad_stream_kernel  512 rows over 160 experts: 236 us, 3.0 TB/s (268 before
+//       neighbouring column blocks met on one XCD); one row 8 us.  Bound by its 4-byte
+//       loads (eight weight rows a lane) and their latency: without the next step's loads
+//       in flight 603 us.
 //
 // Operand layouts (v_mfma_*_16x16x*): lane l holds row (or column) l % 16 and the K
 // slice of lane group l / 16; the accumulator's element v sits at row 4 (l/16) + v,
@@ -397,13 +398,24 @@ __device__ __forceinline__ void grad_tiles(const ProductArgs& p, int g, int r0, 
     }
 }
 
+// Two neighbouring column blocks share the weight's 128-byte lines: they run on one XCD
+// (workgroup b runs on XCD b % 8), one after the other, so that its L2 fetches a line once.
+// Whole groups go around the XCDs, or, with fewer than eight, ranges of columns.
 __global__ __launch_bounds__(64 * kGWaves) void product_grad_stream_kernel(ProductArgs p, int by_rank) {
     __shared__ float red[kGWaves * 32 * 64];
-    const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
-    if (g < 0) return;
+    const int nx = gridDim.x, lin = blockIdx.y * nx + blockIdx.x;
+    int x = blockIdx.x, y = blockIdx.y;
+    if ((gridDim.y & 7) == 0) {
+        x = (lin >> 3) % nx;
+        y = (lin >> 3) / nx * 8 + (lin & 7);
+    } else if ((nx & 7) == 0) {
+        x = (x & 7) * (nx >> 3) + (x >> 3);
+    }
+    const int g = by_rank ? nth_group(p, y) : y;
+    if (g < 0 || g >= p.G) return;
     int rb, re;
     group_rows(p, g, rb, re);
-    const int k0 = blockIdx.x * 128;
+    const int k0 = x * 128;
     for (int r0 = rb; r0 < re;) {
         if (re - r0 > 16) { grad_tiles<2>(p, g, r0, re, k0, red); r0 += 32; }
         else { grad_tiles<1>(p, g, r0, re, k0, red); r0 += 16; }
@@ -412,7 +424,7 @@ __global__ __launch_bounds__(64 * kGWaves) void product_grad_stream_kernel(Produ
 
 hipError_t launch_product_grad_stream(const ProductArgs& p, hipStream_t s) {
     const int groups = min(p.G, p.M);
-    const dim3 grid((p.K + 127) / 128, groups);
+    const dim3 grid((p.K + 127) / 128, groups < 8 ? groups : (groups + 7) & ~7);
     const int by_rank = p.M < p.G ? 1 : 0;
     hipLaunchKernelGGL(product_grad_stream_kernel, grid, dim3(64 * kGWaves), 0, s, p, by_rank);
     return hipGetLastError();
@@ -424,22 +436,28 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // Rows a group (M / G, an upper bound of their mean) up to which the weight is streamed
 // past the tokens instead of multiplied in 256 x 256 tiles.  Measured on 64 groups of
 // 2048 x 4096, us streamed against tiled: W4A16 77 / 110 at 16 rows, 124 / 119 at 32;
-// W4A4 59 / 72 and 96 / 75; backward 127 / 135 and 179 / 164.  Tiles that leave most of
-// the card idle lose for longer (one group of 4096 x 4096: W4A16 38 / 54 at 128 rows,
-// 74 / 85 at 256; W4A4 24 / 27 at 128; backward 63 / 75 at 128; eight groups of 2048 x
-// 4096 cross at about 32 again): the bound grows with the CUs that the tiles of one row
-// block leave four times over.
-static bool streamed(const ProductArgs& p, int rows, int width, int cus) {
-    const int64_t tiles = (int64_t)p.G * ((width + 255) / 256);
+// W4A4 59 / 72 and 96 / 75.  Tiles that leave most of the card idle lose for longer (one
+// group of 4096 x 4096: W4A16 38 / 54 at 128 rows, 74 / 85 at 256; W4A4 24 / 27 at 128;
+// eight groups of 2048 x 4096 cross at about 32 again): the bound grows with the CUs that
+// the tiles of one row block leave four times over.
+static bool streamed(const ProductArgs& p, int rows, int cus) {
+    const int64_t tiles = (int64_t)p.G * ((p.N + 255) / 256);
     const int64_t idle = cus / (4 * tiles);
     return p.M <= p.G * rows * (idle > 1 ? idle : 1) || !tiles_reach(p);
 }
 
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
-    return streamed(p, p.a_s ? 20 : 24, p.N, cus) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
+    return streamed(p, p.a_s ? 20 : 24, cus) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
 }
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
-    return streamed(p, 24, p.K, cus) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, cus, s);
+    // The gradient's crossings, us streamed against tiled: 64 groups of 2048 x 4096 154 / 171
+    // at 32 rows a group, 197 / 175 at 47 (16 groups: 47 / 50 at 40, 64 / 52 at 64); with the
+    // tiles of one row block on half the card (eight groups) 43 / 49 at 90, on a quarter
+    // or less 39 / 47 at 100 and 58 / 54 at 150 (four groups), 65 / 86 at 128 (one of 4096 x
+    // 4096).
+    const int64_t tiles = (int64_t)p.G * ((p.K + 255) / 256), idle = min((int64_t)4, cus / tiles);
+    if (p.M <= p.G * 36 * (idle > 1 ? idle : 1) || !tiles_reach(p)) return launch_product_grad_stream(p, s);
+    return launch_product_grad_tiles(p, cus, s);
 }
 
 }  // namespace moe
