@@ -33,10 +33,6 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-// the same at any byte address: global loads and stores of gfx950 need no alignment
-// (the compiler keeps one instruction); rows of any stride use them
-typedef u32x4_t u32x4_any_t __attribute__((aligned(1)));
-typedef u32x2_t u32x2_any_t __attribute__((aligned(1)));
 
 namespace moe {
 

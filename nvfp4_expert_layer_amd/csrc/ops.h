@@ -4,6 +4,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+// Four and two dwords at any byte address: global loads and stores of gfx950 need no
+// alignment (the compiler keeps one instruction); rows of any stride use them.
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(1)));
+
 namespace moe {
 
 enum { kBF16 = 0, kF16 = 1, kF32 = 2, kU8 = 3 };       // moe_dtype
