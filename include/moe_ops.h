@@ -18,7 +18,9 @@
  *   - Row strides are in elements and at least the row's width; elements of a row
  *     are contiguous.  Rows of any stride and base address that keep their
  *     elements aligned are taken, except where a call asks for more.
- *   - Outputs must not overlap inputs or each other (INVALID_ARG).
+ *   - Outputs must not overlap inputs or each other (INVALID_ARG).  Rows may take
+ *     different columns of one buffer: strided tensors whose rows interleave are told
+ *     apart by their columns modulo the greatest common divisor of their row strides.
  *   - Sums, products and dot products are fp32; each result is rounded once to its
  *     type.  No atomic decides an order: equal inputs give equal bits.
  *   - ARCH when the current device is not gfx950.

@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <numeric>
+
 #include "kernels.h"
 #include "ops.h"
 #include "status.h"
@@ -18,29 +20,46 @@ using moe::ok;
 
 bool misaligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-// A byte range of device memory that a call reads or writes (empty when p is NULL).
+// Device memory that a call reads or writes: `rows` pieces of `width` bytes, `stride`
+// bytes apart (nothing when p is NULL or a count is 0).
 struct Range {
     const char* what;
     const void* p;
-    size_t bytes;
+    uint64_t rows, width, stride;
     bool written;
 };
 
-// Bytes from the first to the last element of rows x width with a row stride.
-size_t extent(int64_t rows, int64_t width, int64_t stride, int elem) {
-    return rows > 0 && width > 0 ? (size_t)(((rows - 1) * stride + width) * elem) : 0;
+Range dense(const char* what, const void* p, uint64_t bytes, bool written) {
+    return Range{what, p, 1, bytes, 0, written};
+}
+
+// rows x width elements with a row stride (of one row, the stride is not looked at).
+Range strided(const char* what, const void* p, int64_t rows, int64_t width, int64_t stride, int elem, bool written) {
+    return Range{what, p, (uint64_t)rows, (uint64_t)(width * elem), rows > 1 ? (uint64_t)(stride * elem) : 0, written};
+}
+
+// Whether two ranges share a byte.  Two views of one buffer may take different columns of
+// it: modulo the greatest common divisor g of the strides every row of x lies at the same
+// place, and so does every row of y; where these places are apart no byte is shared.  Of
+// equal strides, or where one range is a single piece, this decides exactly; of others
+// the ranges count as overlapping when their ends do.
+bool overlap(const Range& x, const Range& y) {
+    if (!x.p || !y.p || !x.rows || !y.rows || !x.width || !y.width) return false;
+    const uint64_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    if (a >= b + (y.rows - 1) * y.stride + y.width || b >= a + (x.rows - 1) * x.stride + x.width) return false;
+    const uint64_t g = std::gcd(x.stride, y.stride);
+    if (g == 0) return true;
+    const uint64_t at = a <= b ? (b - a) % g : (g - (a - b) % g) % g;      // y's place, x at 0
+    return at < x.width || at + y.width > g;
 }
 
 // No written range may overlap another.
 template <size_t N>
 int check_overlap(const Range (&r)[N]) {
     for (size_t i = 0; i < N; ++i)
-        for (size_t j = i + 1; j < N; ++j) {
-            if (!(r[i].written || r[j].written) || !r[i].p || !r[j].p || !r[i].bytes || !r[j].bytes) continue;
-            const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].p), y = reinterpret_cast<uintptr_t>(r[j].p);
-            if (x < y + r[j].bytes && y < x + r[i].bytes)
+        for (size_t j = i + 1; j < N; ++j)
+            if ((r[i].written || r[j].written) && overlap(r[i], r[j]))
                 return fail(MOE_NVFP4_ERR_INVALID_ARG, "%s overlaps %s", r[i].what, r[j].what);
-        }
     return MOE_NVFP4_OK;
 }
 
@@ -111,10 +130,9 @@ int combine_rows(const moe_dispatch_problem* p, const int32_t* inv, const float*
         (st = check_rows("out", out, p->num_tokens, p->width, out_stride, p->dtype)))
         return st;
     const int eb = moe::dtype_bytes(p->dtype);
-    const Range r[] = {{"out", out, extent(p->num_tokens, p->width, out_stride, eb), true},
-                       {"rows", rows, extent(pairs(p), p->width, rows_stride, eb), false},
-                       {"inv", inv, (size_t)pairs(p) * 4, false},
-                       {"weights", weights, (size_t)pairs(p) * 4, false}};
+    const Range r[] = {strided("out", out, p->num_tokens, p->width, out_stride, eb, true),
+                       strided("rows", rows, pairs(p), p->width, rows_stride, eb, false),
+                       dense("inv", inv, pairs(p) * 4, false), dense("weights", weights, pairs(p) * 4, false)};
     if ((st = check_overlap(r))) return st;
     int dev;
     if ((st = current_arch_ok(&dev))) return st;
@@ -183,14 +201,14 @@ int moe_dispatch(const moe_dispatch_problem* p, const int32_t* ids, const void* 
     if (need && misaligned(workspace, 4)) return fail(MOE_NVFP4_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
     const int eb = moe::dtype_bytes(p->dtype);
     const size_t np = (size_t)pairs(p), L = (size_t)p->num_local_experts;
-    const Range r[] = {{"rows", rows, extent(pairs(p), p->width, rows_stride, eb), true},
-                       {"counts", counts, L * 4, true},
-                       {"offsets", offsets, (L + 1) * 4, true},
-                       {"perm", perm, np * 4, true},
-                       {"inv", inv, np * 4, true},
-                       {"workspace", need ? workspace : nullptr, need, true},
-                       {"x", x, extent(p->num_tokens, p->width, x_stride, eb), false},
-                       {"ids", ids, np * 4, false}};
+    const Range r[] = {strided("rows", rows, pairs(p), p->width, rows_stride, eb, true),
+                       dense("counts", counts, L * 4, true),
+                       dense("offsets", offsets, (L + 1) * 4, true),
+                       dense("perm", perm, np * 4, true),
+                       dense("inv", inv, np * 4, true),
+                       dense("workspace", workspace, need, true),
+                       strided("x", x, p->num_tokens, p->width, x_stride, eb, false),
+                       dense("ids", ids, np * 4, false)};
     if ((st = check_overlap(r))) return st;
     int dev;
     if ((st = current_arch_ok(&dev))) return st;
@@ -241,12 +259,12 @@ int moe_combine_backward(const moe_dispatch_problem* p, const int32_t* inv, cons
     if (drows && (st = check_rows("drows", drows, pairs(p), p->width, drows_stride, p->dtype))) return st;
     const int eb = moe::dtype_bytes(p->dtype);
     const size_t pb = (size_t)pairs(p) * 4;
-    const Range r[] = {{"drows", drows, extent(pairs(p), p->width, drows_stride, eb), true},
-                       {"dweights", dweights, pb, true},
-                       {"rows", dweights ? rows : nullptr, extent(pairs(p), p->width, rows_stride, eb), false},
-                       {"dout", dout, extent(p->num_tokens, p->width, dout_stride, eb), false},
-                       {"inv", inv, pb, false},
-                       {"weights", weights, pb, false}};
+    const Range r[] = {strided("drows", drows, pairs(p), p->width, drows_stride, eb, true),
+                       dense("dweights", dweights, pb, true),
+                       strided("rows", dweights ? rows : nullptr, pairs(p), p->width, rows_stride, eb, false),
+                       strided("dout", dout, p->num_tokens, p->width, dout_stride, eb, false),
+                       dense("inv", inv, pb, false),
+                       dense("weights", weights, pb, false)};
     if ((st = check_overlap(r))) return st;
     int dev;
     if ((st = current_arch_ok(&dev))) return st;
@@ -275,9 +293,9 @@ int moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t R, int32_t C, int64
     if (st) return st;
     if ((st = check_mxfp4_tensor(R, C, codes, scales))) return st;
     if ((st = check_rows("x", x, R, C, x_stride, dtype))) return st;
-    const Range r[] = {{"codes", codes, (size_t)R * C / 2, true},
-                       {"scales", scales, (size_t)R * C / 32, true},
-                       {"x", x, extent(R, C, x_stride, moe::dtype_bytes(dtype)), false}};
+    const Range r[] = {dense("codes", codes, (size_t)R * C / 2, true),
+                       dense("scales", scales, (size_t)R * C / 32, true),
+                       strided("x", x, R, C, x_stride, moe::dtype_bytes(dtype), false)};
     if ((st = check_overlap(r))) return st;
     int dev;
     if ((st = current_arch_ok(&dev))) return st;
@@ -293,9 +311,9 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R,
     if (st) return st;
     if ((st = check_mxfp4_tensor(R, C, codes, scales))) return st;
     if ((st = check_rows("out", out, R, C, out_stride, dtype))) return st;
-    const Range r[] = {{"out", out, extent(R, C, out_stride, moe::dtype_bytes(dtype)), true},
-                       {"codes", codes, (size_t)R * C / 2, false},
-                       {"scales", scales, (size_t)R * C / 32, false}};
+    const Range r[] = {strided("out", out, R, C, out_stride, moe::dtype_bytes(dtype), true),
+                       dense("codes", codes, (size_t)R * C / 2, false),
+                       dense("scales", scales, (size_t)R * C / 32, false)};
     if ((st = check_overlap(r))) return st;
     int dev;
     if ((st = current_arch_ok(&dev))) return st;
@@ -324,12 +342,12 @@ int moe_mxfp4_product(const moe_product_problem* p, const void* a, const uint8_t
     if (misaligned(a, 16)) return fail(MOE_NVFP4_ERR_INVALID_ARG, "a must be 16-byte aligned");
     if ((st = check_rows("out", out, M, N, out_stride, out_dtype))) return st;
     const size_t wn = (size_t)p->groups * N;
-    const Range r[] = {{"out", out, extent(M, N, out_stride, moe::dtype_bytes(out_dtype)), true},
-                       {"a", a, a_scales ? (size_t)M * K / 2 : extent(M, K, a_stride, 2), false},
-                       {"a_scales", a_scales, (size_t)M * K / 32, false},
-                       {"w", w, wn * K / 2, false},
-                       {"w_scales", w_scales, wn * K / 32, false},
-                       {"offsets", offsets, ((size_t)p->groups + 1) * 4, false}};
+    const Range r[] = {strided("out", out, M, N, out_stride, moe::dtype_bytes(out_dtype), true),
+                       a_scales ? dense("a", a, (size_t)M * K / 2, false) : strided("a", a, M, K, a_stride, 2, false),
+                       dense("a_scales", a_scales, (size_t)M * K / 32, false),
+                       dense("w", w, wn * K / 2, false),
+                       dense("w_scales", w_scales, wn * K / 32, false),
+                       dense("offsets", offsets, ((size_t)p->groups + 1) * 4, false)};
     if ((st = check_overlap(r))) return st;
     int dev, cus;
     if ((st = current_arch_ok(&dev))) return st;
@@ -352,11 +370,11 @@ int moe_mxfp4_product_backward(const moe_product_problem* p, const void* dout, i
         (st = check_rows("drows", drows, M, K, drows_stride, drows_dtype)))
         return st;
     const size_t wn = (size_t)p->groups * N;
-    const Range r[] = {{"drows", drows, extent(M, K, drows_stride, moe::dtype_bytes(drows_dtype)), true},
-                       {"dout", dout, extent(M, N, dout_stride, 2), false},
-                       {"w", w, wn * K / 2, false},
-                       {"w_scales", w_scales, wn * K / 32, false},
-                       {"offsets", offsets, ((size_t)p->groups + 1) * 4, false}};
+    const Range r[] = {strided("drows", drows, M, K, drows_stride, moe::dtype_bytes(drows_dtype), true),
+                       strided("dout", dout, M, N, dout_stride, 2, false),
+                       dense("w", w, wn * K / 2, false),
+                       dense("w_scales", w_scales, wn * K / 32, false),
+                       dense("offsets", offsets, ((size_t)p->groups + 1) * 4, false)};
     if ((st = check_overlap(r))) return st;
     int dev, cus;
     if ((st = current_arch_ok(&dev))) return st;
