@@ -138,16 +138,17 @@ def moe_dispatch(problem, ids, x, counts, offsets, perm, inv, rows, workspace, s
     """Sorts the pairs of ids int32 [T, k] by local expert and gathers the token rows.
     x [T, d] -> rows [T k, d] (both None: the plan alone); counts int32 [L], offsets
     int32 [L + 1], perm int32 [T k], inv int32 [T, k] (each may be None); workspace
-    uint8 (moe_dispatch_workspace_size bytes).  perm and rows past the kept pairs
-    stay as they were.  Returns rows."""
+    uint8 (moe_dispatch_workspace_size bytes; may be None where that is 0).  perm and
+    rows past the kept pairs stay as they were.  Returns rows."""
     p, i32 = problem, torch.int32
     T, k, L, dt = p.num_tokens, p.top_k, p.num_local_experts, (_TORCH[p.dtype],)
+    have = 0 if workspace is None else workspace.numel()
     (px, xs, pr, rs), (pi, pc, po, pp, pv, pw), dev = _tensors(
         ((x, "x", dt, (T, p.width)), (rows, "rows", dt, (T * k, p.width))),
         ((ids, "ids", i32, (T, k)), (counts, "counts", i32, (L,)), (offsets, "offsets", i32, (L + 1,)),
          (perm, "perm", i32, (T * k,)), (inv, "inv", i32, (T, k)),
-         (workspace, "workspace", torch.uint8, (workspace.numel(),))))
-    _check(_lib().moe_dispatch(ctypes.byref(p), pi, px, xs, pc, po, pp, pv, pr, rs, pw, workspace.numel(),
+         (workspace, "workspace", torch.uint8, (have,))))
+    _check(_lib().moe_dispatch(ctypes.byref(p), pi, px, xs, pc, po, pp, pv, pr, rs, pw, have,
                                _stream_of(stream, dev)))
     return rows
 
