@@ -439,15 +439,19 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // W4A4 59 / 72 and 96 / 75.  Tiles that leave most of the card idle lose for longer (one
 // group of 4096 x 4096: W4A16 38 / 54 at 128 rows, 74 / 85 at 256; W4A4 24 / 27 at 128;
 // eight groups of 2048 x 4096 cross at about 32 again): the bound grows with the CUs that
-// the tiles of one row block leave four times over.
-static bool streamed(const ProductArgs& p, int rows, int cus) {
+// the tiles of one row block leave four times over, up to `most` times.  There the card is
+// idle either way and the streaming kernels' passes over 32 rows, one after another, cost
+// as much as a tile (one group, K = 4096, 16, 256 and 512 outputs alike): W4A16 73 / 84 at
+// 256 rows, 150 / 83 at 512, 450 / 84 at 1536; W4A4 23 / 27 at 128, 45 / 33 at 256, 172 / 33
+// at 1024 (K = 1024: W4A16 24 / 28 at 256, 47 / 28 at 512; W4A4 18 / 13 at 256).
+static bool streamed(const ProductArgs& p, int rows, int most, int cus) {
     const int64_t tiles = (int64_t)p.G * ((p.N + 255) / 256);
-    const int64_t idle = cus / (4 * tiles);
+    const int64_t idle = min((int64_t)most, cus / (4 * tiles));
     return p.M <= p.G * rows * (idle > 1 ? idle : 1) || !tiles_reach(p);
 }
 
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
-    return streamed(p, p.a_s ? 20 : 24, cus) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
+    return (p.a_s ? streamed(p, 20, 8, cus) : streamed(p, 24, 12, cus)) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
 }
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
     // The gradient's crossings, us streamed against tiled: 64 groups of 2048 x 4096 154 / 171
