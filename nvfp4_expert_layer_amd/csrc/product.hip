@@ -444,24 +444,35 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // as much as a tile (one group, K = 4096, 16, 256 and 512 outputs alike): W4A16 73 / 84 at
 // 256 rows, 150 / 83 at 512, 450 / 84 at 1536; W4A4 23 / 27 at 128, 45 / 33 at 256, 172 / 33
 // at 1024 (K = 1024: W4A16 24 / 28 at 256, 47 / 28 at 512; W4A4 18 / 13 at 256).
-static bool streamed(const ProductArgs& p, int rows, int most, int cus) {
-    const int64_t tiles = (int64_t)p.G * ((p.N + 255) / 256);
-    const int64_t idle = min((int64_t)most, cus / (4 * tiles));
+static bool streamed(const ProductArgs& p, int cus) {
+    const int rows = p.a_s ? 20 : 24;
+    const int64_t most = p.a_s ? 8 : 12, tiles = (int64_t)p.G * ((p.N + 255) / 256);
+    const int64_t idle = min(most, cus / (4 * tiles));
     return p.M <= p.G * rows * (idle > 1 ? idle : 1) || !tiles_reach(p);
+}
+// The gradient's crossings, us streamed against tiled: 64 groups of 2048 x 4096 154 / 171
+// at 32 rows a group, 197 / 175 at 47 (16 groups: 47 / 50 at 40, 64 / 52 at 64); with the
+// tiles of one row block on half the card (eight groups) 43 / 49 at 90, on a quarter
+// or less 39 / 47 at 100 and 58 / 54 at 150 (four groups), 65 / 86 at 128 (one of 4096 x
+// 4096).
+static bool grad_streamed(const ProductArgs& p, int cus) {
+    const int64_t tiles = (int64_t)p.G * ((p.K + 255) / 256), idle = min((int64_t)4, cus / tiles);
+    return p.M <= p.G * 36 * (idle > 1 ? idle : 1) || !tiles_reach(p);
 }
 
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
-    return (p.a_s ? streamed(p, 20, 8, cus) : streamed(p, 24, 12, cus)) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
+    return streamed(p, cus) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
 }
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
-    // The gradient's crossings, us streamed against tiled: 64 groups of 2048 x 4096 154 / 171
-    // at 32 rows a group, 197 / 175 at 47 (16 groups: 47 / 50 at 40, 64 / 52 at 64); with the
-    // tiles of one row block on half the card (eight groups) 43 / 49 at 90, on a quarter
-    // or less 39 / 47 at 100 and 58 / 54 at 150 (four groups), 65 / 86 at 128 (one of 4096 x
-    // 4096).
-    const int64_t tiles = (int64_t)p.G * ((p.K + 255) / 256), idle = min((int64_t)4, cus / tiles);
-    if (p.M <= p.G * 36 * (idle > 1 ? idle : 1) || !tiles_reach(p)) return launch_product_grad_stream(p, s);
-    return launch_product_grad_tiles(p, cus, s);
+    return grad_streamed(p, cus) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, cus, s);
 }
 
 }  // namespace moe
+
+int moe_internal_product_streams(int M, int N, int K, int G, int64_t stride, int mx, int backward, int cus) {
+    moe::ProductArgs p{};
+    const uint8_t scales = 0;
+    p.M = M; p.N = N; p.K = K; p.G = G; p.as = stride;
+    p.a_s = mx ? &scales : nullptr;
+    return backward ? moe::grad_streamed(p, cus) : moe::streamed(p, cus);
+}
