@@ -126,7 +126,11 @@ int moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t R,
 /* Rows sorted by group (expert) times each group's weight.  Group g owns rows
  * [offsets[g], offsets[g+1]) (device int32 [groups+1], e.g. moe_dispatch's;
  * clamped to [0, rows]; must not decrease); offsets NULL with groups == 1: all
- * rows.  Rows of no group are neither read nor written. */
+ * rows.  Rows of no group are neither read nor written.
+ *
+ * Every scale byte counts as the format says, subnormal values too, with one bound:
+ * W4A16 and the gradient hold weights in bf16, where a value of 2^128 or more (codes
+ * from 4 on under s = 253, from 2 on under 254) is Inf. */
 typedef struct {
     int32_t rows;      /* M >= 0: rows of the buffers (an upper bound of the groups' rows) */
     int32_t n;         /* N: 1..65536, output features                                      */
