@@ -132,7 +132,8 @@ int moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t R,
  * W4A16 and the gradient hold weights in bf16, where a value of 2^128 or more (codes
  * from 4 on under s = 253, from 2 on under 254) is Inf. */
 typedef struct {
-    int32_t rows;      /* M >= 0: rows of the buffers (an upper bound of the groups' rows) */
+    int32_t rows;      /* M: 0..2^27, rows of the buffers (an upper bound of the groups'    */
+                       /* rows; M / G decides the kernel, so a near bound is the faster)    */
     int32_t n;         /* N: 1..65536, output features                                      */
     int32_t k;         /* K: a multiple of 32, 32..65536, the reduction                     */
     int32_t groups;    /* G: 1..1024                                                        */

@@ -83,7 +83,7 @@ hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t 
 }  // namespace moe
 
 // Whether a product (or its gradient) takes the streaming kernels (1) or the tiles (0): the
-// launches' own rule, device-free.  Exported so that the tests can say which kernel their
-// shapes reach.
+// launches' own rule, device-free, for sizes that the product takes.  Exported so that the
+// tests can say which kernel their shapes reach.
 extern "C" int moe_internal_product_streams(int M, int N, int K, int G, int64_t stride, int mx, int backward,
                                             int cus);

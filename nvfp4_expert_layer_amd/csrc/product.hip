@@ -444,6 +444,9 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // as much as a tile (one group, K = 4096, 16, 256 and 512 outputs alike): W4A16 73 / 84 at
 // 256 rows, 150 / 83 at 512, 450 / 84 at 1536; W4A4 23 / 27 at 128, 45 / 33 at 256, 172 / 33
 // at 1024 (K = 1024: W4A16 24 / 28 at 256, 47 / 28 at 512; W4A4 18 / 13 at 256).
+// M is the buffer's: where few of its rows are kept or one group holds many of them the rule
+// can pick the slower kernel (W4A16, 160 experts of 2048 x 4096: 3500 rows 198 / 236 spread
+// evenly, 572 / 324 after a Zipf law; 40 of 320 experts, an eighth of 2048 rows kept, 47 / 71).
 static bool streamed(const ProductArgs& p, int cus) {
     const int rows = p.a_s ? 20 : 24;
     const int64_t most = p.a_s ? 8 : 12, tiles = (int64_t)p.G * ((p.N + 255) / 256);
