@@ -253,3 +253,37 @@ def test_a_workgroup_takes_five_gradient_tiles_or_more(N):
         b, e = int(off[g]), int(off[g + 1])
         if e > b:
             assert torch.equal(out[b:e], dv[b:e] @ values(w.codes[g], w.scales[g])), (g, b, e)
+
+
+@pytest.mark.parametrize("mode", ["w4a16", "w4a4", "backward"])
+@pytest.mark.parametrize("G", [513, 1023, 1024])
+def test_as_many_groups_as_there_can_be(mode, G):
+    """Exact sums, every group."""
+    require_gpu()
+    log(f"tiles {mode} G={G}")
+    gen = torch.Generator(device="cuda").manual_seed(G)
+    N, K = (40, 128) if mode != "backward" else (24, 96)
+    counts = torch.randint(0, 120, (G,), generator=gen, device="cuda")
+    counts[G // 2], counts[G - 1] = 600, 300
+    off = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), counts.cumsum(0)])
+    M = int(off[-1])
+    on_tiles(mode, M, N, K, G)
+    u8 = dict(dtype=torch.uint8, device="cuda", generator=gen)
+    w = nv.MXFP4Weights(torch.randint(0, 256, (G, N, K // 2), **u8), torch.randint(126, 129, (G, N, K // 32), **u8))
+    v = values(w.codes.view(G * N, K // 2), w.scales.view(G * N, K // 32)).view(G, N, K)
+    p, width = nv.make_product_problem(M, N, K, G), N if mode == "backward" else K
+    a = av = torch.randint(-8, 9, (M, width), generator=gen, device="cuda").to(BF)
+    if mode == "w4a4":
+        a = nv.MXFP4Rows(torch.randint(0, 256, (M, K // 2), **u8), torch.randint(126, 129, (M, K // 32), **u8))
+        av = values(a.codes, a.scales)
+    out = torch.full((M, K if mode == "backward" else N), 55.0, device="cuda")
+    if mode == "backward":
+        nv.moe_mxfp4_product_backward(p, a, w, off.int(), out)
+    else:
+        nv.moe_mxfp4_product(p, a, w, off.int(), out)
+    bounds = off.tolist()
+    for g in range(G):
+        b, e = bounds[g], bounds[g + 1]
+        if e > b:
+            want = av[b:e].float() @ (v[g] if mode == "backward" else v[g].t().contiguous())
+            assert torch.equal(out[b:e], want), (g, b, e)
