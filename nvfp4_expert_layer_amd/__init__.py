@@ -385,3 +385,8 @@ from .ops import (BF16, F16, F32, U8, MXFP4Rows, MXFP4Weights, alloc_dispatch_wo
                   moe_dispatch_backward, moe_dispatch_problem, moe_dispatch_workspace_size, moe_mxfp4_dequantize,
                   moe_mxfp4_product, moe_mxfp4_product_backward, moe_mxfp4_quantize, moe_product_problem,
                   quantize_mxfp4_weights)
+# what stands round its products (include/moe_block.h)
+from .block import (ROUTE_SIGMOID, ROUTE_SOFTMAX, MXFP8Rows, alloc_norm_workspace, make_norm_problem,  # noqa: E402
+                    make_route_problem, make_swiglu_problem, moe_mxfp8_dequantize, moe_mxfp8_product,
+                    moe_mxfp8_quantize, moe_norm, moe_norm_backward, moe_norm_problem, moe_norm_workspace_size, moe_route,
+                    moe_route_backward, moe_route_problem, moe_swiglu, moe_swiglu_backward, moe_swiglu_problem)

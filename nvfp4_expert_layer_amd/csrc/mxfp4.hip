@@ -16,41 +16,10 @@
 // fp32 200 us (6.1 TB/s), from bf16 114 us (6.0 TB/s); back to fp32 164 us (222 when no
 // cache holds any of it), to bf16 93 us.
 #include "device_common.h"
+#include "mx_common.h"
 #include "ops.h"
 
 namespace moe {
-
-constexpr int kMx = 32;
-
-// Maximum over a quad of lanes (lanes 4 i .. 4 i + 3).
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-    const uint32_t a = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
-    v = v > a ? v : a;
-    const uint32_t b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);   // quad_perm 2,3,0,1
-    return v > b ? v : b;
-}
-
-// fp32 magnitude bits of eight loaded elements: the largest (integers order as the
-// magnitudes do; Inf and NaN are above every finite value).
-template <int DT>
-__device__ __forceinline__ uint32_t top_bits(const uint32_t (&w)[DT == kF32 ? 8 : 4]) {
-    uint32_t m = 0;
-    if constexpr (DT == kF32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-        return m;
-    } else {
-        uint32_t h = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m = max(m, w[i] & 0x7FFFu);
-            h = max(h, w[i] & 0x7FFF0000u);
-        }
-        if constexpr (DT == kBF16) return max(h, m << 16);
-        m = max(m, h >> 16);
-        return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)m));
-    }
-}
 
 // Eight elements times 2^-(exponent of scale) -> eight E2M1 codes.
 template <int DT>
