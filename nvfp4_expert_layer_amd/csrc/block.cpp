@@ -340,9 +340,9 @@ int moe_mxfp8_product(const moe_product_problem* p, const uint8_t* a, const uint
     if ((st = cu_count(dev, &cus))) return st;
     moe::ProductArgs g{};
     g.M = p->rows; g.N = p->n; g.K = p->k; g.G = p->groups;
-    g.a = a; g.a_s = a_scales; g.as = K; g.w = w; g.w_s = w_scales; g.offsets = offsets;
+    g.a = a; g.a_s = a_scales; g.a8 = true; g.as = K; g.w = w; g.w_s = w_scales; g.offsets = offsets;
     g.out = out; g.out_dtype = out_dtype; g.os = out_stride;
-    st = hip_status(moe::launch_product8(g, cus, static_cast<hipStream_t>(stream)), "MXFP8 product launch");
+    st = hip_status(moe::launch_product(g, cus, static_cast<hipStream_t>(stream)), "MXFP8 product launch");
     return st ? st : ok();
 }
 

@@ -1,5 +1,5 @@
 // Internal interface between the host code of include/moe_block.h (block.cpp) and its
-// gfx950 kernels (topk.hip, norm.hip, swiglu.hip, mxfp8.hip, product8.hip).  Strides are in
+// gfx950 kernels (topk.hip, norm.hip, swiglu.hip, mxfp8.hip; the product: product.hip, product8.hip).  Strides are in
 // elements.
 #pragma once
 #include "ops.h"
@@ -88,8 +88,5 @@ hipError_t launch_mxfp8_quantize(const void* x, int dtype, int64_t R, int C, int
                                  uint8_t* scales, hipStream_t s);
 hipError_t launch_mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int C, int dtype,
                                    void* out, int64_t os, hipStream_t s);
-
-// p.a: MXFP8 codes [M][K], p.a_s their scales
-hipError_t launch_product8(const ProductArgs& p, int cus, hipStream_t s);
 
 }  // namespace moe

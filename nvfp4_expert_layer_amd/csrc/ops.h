@@ -64,8 +64,9 @@ hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
 
 struct ProductArgs {
     int M, N, K, G;
-    const void* a;                // bf16 [M][K] (stride as), or MXFP4 codes [M][K/2]
+    const void* a;                // bf16 [M][K] (stride as), or MXFP4 codes [M][K/2], or MXFP8 codes [M][K]
     const uint8_t* a_s;           // nullptr: bf16 rows
+    bool a8;                      // MXFP8 rows
     int64_t as;
     const uint8_t* w;             // [G][N][K/2]
     const uint8_t* w_s;           // [G][N][K/32]
@@ -77,6 +78,7 @@ struct ProductArgs {
 // cus: compute units of the device; a: the rows, or (backward) dout bf16 [M][N]
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s);
 hipError_t launch_product_tiles(const ProductArgs& p, int cus, hipStream_t s);  // many rows a group
+hipError_t launch_product8_tiles(const ProductArgs& p, int cus, hipStream_t s);
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s);
 hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t s);
 
@@ -84,6 +86,6 @@ hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t 
 
 // Whether a product (or its gradient) takes the streaming kernels (1) or the tiles (0): the
 // launches' own rule, device-free, for sizes that the product takes.  Exported so that the
-// tests can say which kernel their shapes reach.
+// tests can say which kernel their shapes reach.  mx: 0 bf16 rows, 1 MXFP4, 2 MXFP8.
 extern "C" int moe_internal_product_streams(int M, int N, int K, int G, int64_t stride, int mx, int backward,
                                             int cus);

@@ -32,11 +32,45 @@ namespace moe {
 
 constexpr int kSWaves = 4;
 
+// How the rows are held.
+enum RowFormat { kRowsBf16, kRowsMx4, kRowsMx8 };
+
+// A lane's tokens of a block (bf16, MXFP4), or its two pieces of 16 k of a step of 128 (MXFP8:
+// the FP8 operand's lane group lg holds k 16 lg .. + 16 and 64 + 16 lg .. + 16): Q loads of 16
+// bytes, 0 where they pass K.
+template <int FMT> constexpr int kTokenLoads = FMT == kRowsMx4 ? 1 : (FMT == kRowsMx8 ? 2 : 4);
+template <int FMT>
+__device__ __forceinline__ void load_token(const ProductArgs& p, int64_t r, int kb, int lg, bool valid,
+                                           u32x4_t (&v)[kTokenLoads<FMT>]) {
+#pragma unroll
+    for (int q = 0; q < kTokenLoads<FMT>; ++q) {
+        v[q] = u32x4_t{0u, 0u, 0u, 0u};
+        if constexpr (FMT == kRowsMx8) {
+            const int k = (kb - lg) * 32 + 64 * q + 16 * lg;
+            if (valid && k < p.K)
+                v[q] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p.a) + r * p.K + k);
+        } else if (valid && kb * 32 < p.K) {
+            v[q] = FMT == kRowsMx4 ? *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p.a) +
+                                                                       r * (p.K / 2) + (int64_t)kb * 16)
+                                   : *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.a) + r * p.as +
+                                                                       (int64_t)kb * 32 + 8 * q);
+        }
+    }
+}
+
+// One step of 128 k: 16 weight rows' codes and scale byte, 16 tokens.
+template <int FMT>
+__device__ __forceinline__ f32x4_t mfma_mx(const u32x4_t& w, uint32_t ws, const u32x4_t (&a)[kTokenLoads<FMT>],
+                                           uint32_t as, const f32x4_t& c) {
+    if constexpr (FMT == kRowsMx4) return mfma_mx16(w, ws, a[0], as, c);
+    else return mfma_w4a8_16(w, ws, a[0], a[1], as, c);
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 // One pass over the weight tile's K for NT tiles of 16 tokens from row r0.
-template <bool MX, int NR, int NT>
+template <int FMT, int NR, int NT>
 __device__ __forceinline__ void stream_tiles(const ProductArgs& p, int g, int r0, int re, int n0, f32x4_t* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
     const int KB = p.K / 32;
@@ -73,26 +107,13 @@ __device__ __forceinline__ void stream_tiles(const ProductArgs& p, int g, int r0
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int r = r0 + 16 * t + col;
-                const bool v = kv && r < re;
-                if constexpr (MX) {
-                    u32x4_t ac = {0u, 0u, 0u, 0u};
-                    uint32_t as = 0u;
-                    if (v) {
-                        ac = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p.a) +
-                                                               (int64_t)r * (p.K / 2) + (int64_t)kb * 16);
-                        as = p.a_s[(int64_t)r * KB + kb];
-                    }
+                u32x4_t av[kTokenLoads<FMT>];
+                load_token<FMT>(p, r, kb, lg, r < re, av);
+                if constexpr (FMT != kRowsBf16) {
+                    const uint32_t as = kv && r < re ? p.a_s[(int64_t)r * KB + kb] : 0u;
 #pragma unroll
-                    for (int i = 0; i < NR; ++i) acc[i][t] = mfma_mx16(wc[i], ws[i], ac, as, acc[i][t]);
+                    for (int i = 0; i < NR; ++i) acc[i][t] = mfma_mx<FMT>(wc[i], ws[i], av, as, acc[i][t]);
                 } else {
-                    u32x4_t av[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        av[m] = u32x4_t{0u, 0u, 0u, 0u};
-                        if (v)
-                            av[m] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.a) +
-                                                                      (int64_t)r * p.as + (int64_t)kb * 32 + 8 * m);
-                    }
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
                         const float sc = __uint_as_float(ws[i] << 23);
@@ -121,7 +142,7 @@ __device__ __forceinline__ void stream_tiles(const ProductArgs& p, int g, int r0
     }
 }
 
-template <bool MX, int NR>
+template <int FMT, int NR>
 __global__ __launch_bounds__(64 * kSWaves) void product_stream_kernel(ProductArgs p, int by_rank) {
     __shared__ f32x4_t red[kSWaves * NR * 4 * 64];
     const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
@@ -131,9 +152,9 @@ __global__ __launch_bounds__(64 * kSWaves) void product_stream_kernel(ProductArg
     const int n0 = blockIdx.x * 16 * NR;
     for (int r0 = rb; r0 < re;) {
         const int left = re - r0;
-        if (left > 32) { stream_tiles<MX, NR, 4>(p, g, r0, re, n0, red); r0 += 64; }
-        else if (left > 16) { stream_tiles<MX, NR, 2>(p, g, r0, re, n0, red); r0 += 32; }
-        else { stream_tiles<MX, NR, 1>(p, g, r0, re, n0, red); r0 += 16; }
+        if (left > 32) { stream_tiles<FMT, NR, 4>(p, g, r0, re, n0, red); r0 += 64; }
+        else if (left > 16) { stream_tiles<FMT, NR, 2>(p, g, r0, re, n0, red); r0 += 32; }
+        else { stream_tiles<FMT, NR, 1>(p, g, r0, re, n0, red); r0 += 16; }
     }
 }
 
@@ -145,32 +166,22 @@ __global__ __launch_bounds__(64 * kSWaves) void product_stream_kernel(ProductArg
 // ---------------------------------------------------------------------------
 constexpr int kRWaves = 8;
 
-template <bool MX, int KS, int NT, bool S16>
+template <int FMT, int KS, int NT, bool S16>
 __device__ __forceinline__ void resident_tiles(const ProductArgs& p, int g, int r0, int re, int t0, int t1,
                                                f32x4_t* red) {
-    constexpr int TQ = MX ? 1 : 4;                              // 16-byte operands of a block's tokens
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, lg = lane >> 4, KB = p.K / 32;
     const int kb0 = wave * KS * 4 + lg;                         // this lane's block of step s: kb0 + 4 s
-    u32x4_t tok[KS][NT][TQ];
+    u32x4_t tok[KS][NT][kTokenLoads<FMT>];
     uint32_t ts[KS][NT];
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = r0 + 16 * t + col, kb = kb0 + 4 * s;
-            const bool v = r < re && kb < KB;
             ts[s][t] = 0u;
-            if (MX && v) ts[s][t] = p.a_s[(int64_t)r * KB + kb];
-#pragma unroll
-            for (int q = 0; q < TQ; ++q) {
-                tok[s][t][q] = u32x4_t{0u, 0u, 0u, 0u};
-                if (v)
-                    tok[s][t][q] = MX ? *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(p.a) +
-                                                                          (int64_t)r * (p.K / 2) + kb * 16)
-                                      : *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.a) +
-                                                                          r * p.as + kb * 32 + 8 * q);
-            }
+            if (FMT != kRowsBf16 && r < re && kb < KB) ts[s][t] = p.a_s[(int64_t)r * KB + kb];
+            load_token<FMT>(p, r, kb, lg, r < re, tok[s][t]);
         }
     struct Weight {
         u32x4_t c[KS];
@@ -210,9 +221,9 @@ __device__ __forceinline__ void resident_tiles(const ProductArgs& p, int g, int 
         for (int s = 0; s < KS; ++s) {
             uint32_t sb = S16 ? (w.s[s] >> (8 * lg)) & 0xFFu : w.s[s];
             if (kb0 + 4 * s >= KB) sb = 127u;
-            if constexpr (MX) {
+            if constexpr (FMT != kRowsBf16) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) acc[i] = mfma_mx16(w.c[s], sb, tok[s][i][0], ts[s][i], acc[i]);
+                for (int i = 0; i < NT; ++i) acc[i] = mfma_mx<FMT>(w.c[s], sb, tok[s][i], ts[s][i], acc[i]);
             } else {
                 const float sc = __uint_as_float(sb << 23);
 #pragma unroll
@@ -251,7 +262,7 @@ __device__ __forceinline__ void resident_tiles(const ProductArgs& p, int g, int 
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <bool MX, int KS, int MAXT, bool S16>
+template <int FMT, int KS, int MAXT, bool S16>
 __global__ __launch_bounds__(64 * kRWaves) void product_resident_kernel(ProductArgs p, int by_rank, int per_block) {
     __shared__ f32x4_t red[2 * kRWaves * MAXT * 64];
     const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
@@ -261,16 +272,16 @@ __global__ __launch_bounds__(64 * kRWaves) void product_resident_kernel(ProductA
     const int t0 = blockIdx.x * per_block, t1 = min(t0 + per_block, (p.N + 15) / 16);
     for (int r0 = rb; r0 < re;) {
         if (MAXT > 1 && re - r0 > 16) {
-            resident_tiles<MX, KS, MAXT, S16>(p, g, r0, re, t0, t1, red);
+            resident_tiles<FMT, KS, MAXT, S16>(p, g, r0, re, t0, t1, red);
             r0 += 16 * MAXT;
         } else {
-            resident_tiles<MX, KS, 1, S16>(p, g, r0, re, t0, t1, red);
+            resident_tiles<FMT, KS, 1, S16>(p, g, r0, re, t0, t1, red);
             r0 += 16;
         }
     }
 }
 
-template <bool MX, int KS, int MAXT>
+template <int FMT, int KS, int MAXT>
 static void launch_resident(const ProductArgs& p, int cus, int groups, int by_rank, hipStream_t s) {
     // tiles a workgroup: as many as leave one workgroup a CU, 16 at most. Experts of 2048 x
     // 4096: 8 rows over 320 take 11.4 us, with two workgroups a CU 14.0; 512 rows over 160
@@ -283,30 +294,31 @@ static void launch_resident(const ProductArgs& p, int cus, int groups, int by_ra
     const bool s16 = p.K % (128 * KS) == 0 && (p.K / 32) % part == 0 &&
                      (reinterpret_cast<uintptr_t>(p.w_s) & (part - 1)) == 0;
     if (s16)
-        hipLaunchKernelGGL((product_resident_kernel<MX, KS, MAXT, true>), grid, dim3(64 * kRWaves), 0, s, p, by_rank,
+        hipLaunchKernelGGL((product_resident_kernel<FMT, KS, MAXT, true>), grid, dim3(64 * kRWaves), 0, s, p, by_rank,
                            per);
     else
-        hipLaunchKernelGGL((product_resident_kernel<MX, KS, MAXT, false>), grid, dim3(64 * kRWaves), 0, s, p, by_rank,
+        hipLaunchKernelGGL((product_resident_kernel<FMT, KS, MAXT, false>), grid, dim3(64 * kRWaves), 0, s, p, by_rank,
                            per);
 }
 
-template <bool MX>
+template <int FMT>
 static hipError_t launch_stream(const ProductArgs& p, int cus, hipStream_t s) {
     const int groups = min(p.G, p.M);                           // at most so many hold rows
     const int by_rank = p.M < p.G ? 1 : 0;
     // (a variant for 16 tokens alone, with fewer registers, was no faster at any row count)
-    if (p.K <= 1024) launch_resident<MX, 1, 2>(p, cus, groups, by_rank, s);
-    else if (p.K <= 2048) launch_resident<MX, 2, 2>(p, cus, groups, by_rank, s);
-    else if (p.K <= 4096) launch_resident<MX, 4, 2>(p, cus, groups, by_rank, s);
-    else if (MX && p.K <= 8192) launch_resident<true, 8, 1>(p, cus, groups, by_rank, s);
+    if (p.K <= 1024) launch_resident<FMT, 1, 2>(p, cus, groups, by_rank, s);
+    else if (p.K <= 2048) launch_resident<FMT, 2, 2>(p, cus, groups, by_rank, s);
+    else if (p.K <= 4096) launch_resident<FMT, 4, 2>(p, cus, groups, by_rank, s);
+    else if (FMT != kRowsBf16 && p.K <= 8192) launch_resident<FMT == kRowsBf16 ? kRowsMx4 : FMT, 8, 1>(p, cus, groups, by_rank, s);
     else
-        hipLaunchKernelGGL((product_stream_kernel<MX, 1>), dim3((p.N + 15) / 16, groups), dim3(64 * kSWaves), 0, s, p,
+        hipLaunchKernelGGL((product_stream_kernel<FMT, 1>), dim3((p.N + 15) / 16, groups), dim3(64 * kSWaves), 0, s, p,
                            by_rank);
     return hipGetLastError();
 }
 
 hipError_t launch_product_stream(const ProductArgs& p, int cus, hipStream_t s) {
-    return p.a_s ? launch_stream<true>(p, cus, s) : launch_stream<false>(p, cus, s);
+    if (p.a8) return launch_stream<kRowsMx8>(p, cus, s);
+    return p.a_s ? launch_stream<kRowsMx4>(p, cus, s) : launch_stream<kRowsBf16>(p, cus, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -464,7 +476,8 @@ static bool grad_streamed(const ProductArgs& p, int cus) {
 }
 
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s) {
-    return streamed(p, cus) ? launch_product_stream(p, cus, s) : launch_product_tiles(p, cus, s);
+    if (streamed(p, cus)) return launch_product_stream(p, cus, s);
+    return p.a8 ? launch_product8_tiles(p, cus, s) : launch_product_tiles(p, cus, s);
 }
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
     return grad_streamed(p, cus) ? launch_product_grad_stream(p, s) : launch_product_grad_tiles(p, cus, s);
@@ -477,5 +490,6 @@ int moe_internal_product_streams(int M, int N, int K, int G, int64_t stride, int
     const uint8_t scales = 0;
     p.M = M; p.N = N; p.K = K; p.G = G; p.as = stride;
     p.a_s = mx ? &scales : nullptr;
+    p.a8 = mx == 2;
     return backward ? moe::grad_streamed(p, cus) : moe::streamed(p, cus);
 }

@@ -1,98 +1,313 @@
-// Products of MXFP8 rows with MXFP4 weights (W4A8, gfx950), rows sorted by group:
-//   out[r][n] = sum_k a[r][k] w[g(r)][n][k]
-// v_mfma_scale_f32_16x16x128_f8f6f4 takes both formats as they lie in memory.  Operand
-// layouts (checked on the device): of the 128 k of a step, lane l of the FP4 operand holds the
-// 32 codes of block l / 16 of row l % 16; of the FP8 operand the 16 codes from 16 (l / 16) and
-// the 16 from 64 + 16 (l / 16) of column l % 16; both give the scale of block l / 16.  The
-// accumulator's element v sits at row 4 (l / 16) + v, column l % 16.  The weight is the row
-// operand, tokens are columns, so a lane ends with four consecutive outputs of one token.
+// Products of MXFP8 rows with MXFP4 weights (W4A8) in tiles, for many rows a group (gfx950).
+// A tile is 256 rows of one group x 256 outputs; eight waves of 64 rows x 128 outputs, one
+// workgroup a CU; the operands come straight from global memory to LDS.
+//
+//   32x32x64 scaled MFMAs take both formats as they lie in memory (half the rate of FP4 x FP4,
+//   twice bf16's).  The rows' ring holds two stages of 128 k, the weight's two of 256 k: a full
+//   128-byte line of a row each.  The matrix cores need 2 x 512 cycles a SIMD and stage; LDS
+//   gives 128 KB a stage to the waves, which the 64 x 128 wave tiles keep under their time
+//   (128 x 64: 160 KB).
 //
 // The unit adds the products of eight neighbouring k aligned to the largest, without the bits
-// below 2^-13 of it (checked on the device); everything beyond is fp32.
-#include "block.h"
-#include "product_common.h"
+// below 2^-13 of it (checked on the device: rows spread over E4M3's whole range lose up to
+// 2^-11 of their largest product); everything beyond is fp32.
+#include "product_tiles_common.h"
 
 namespace moe {
 
-__device__ __forceinline__ f32x4_t mfma_w4a8_16(const u32x4_t& w, uint32_t ws, const u32x4_t& lo, const u32x4_t& hi,
-                                                uint32_t as, const f32x4_t& c) {
-    const i32x8_t a = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(w), a, c, 4, 0, 0, (int)ws, 0, (int)as);
+constexpr int k8Part = 256 * 128;                          // a slot: 128 k of the rows, 256 k of the weight
+constexpr int k8OffW = 2 * k8Part, k8OffS = 4 * k8Part;    // rows [2] | weight [2] | scales [2] | ...
+// Scales of 512 k of both operands, or (rows of scales that are not aligned to dwords) of 256 k,
+// each byte in a dword of its own.
+constexpr int k8Pair = 2 * scale_bytes(true, 16), k8Bytes = 2 * scale_bytes(false, 8);
+// ... | waves' staging [8] | table.  Without aligned scales the stages take all 160 KB: one
+// tile a workgroup, staged and looked up in the stages' place.
+constexpr int k8OffStage = k8OffS + 2 * k8Pair, k8OffTable = k8OffStage + kTWaves * kWaveStage / 2;
+constexpr int w4a8_lds(bool aligned) { return aligned ? k8OffTable + kTable : k8OffS + 2 * k8Bytes; }
+
+template <int OPSEL>
+__device__ __forceinline__ f32x16_t mfma_w4a8_32(const u32x4_t& w, uint32_t ws, const u32x4_t& lo, const u32x4_t& hi,
+                                                 uint32_t as, const f32x16_t& c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(w), mx8_operand(lo, hi), c, 4, 0, OPSEL, (int)ws,
+                                                           OPSEL, (int)as);
 }
 
-constexpr int kSWaves = 4;
+// A workgroup takes tiles one after another: while a tile's last stages are multiplied the next
+// tile's first ones are loaded, and its outputs leave while those land.
+// ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales).
+template <bool ALIGNED>
+__global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
+    constexpr int kSlotS = ALIGNED ? k8Pair : k8Bytes, kScales = kSlotS / 2;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int wm = wave >> 1, wn = wave & 1;             // rows 64 wm .. +64, outputs 128 wn .. +128
+    const int NT = (p.N + kTN - 1) / kTN, KB = p.K / 32, nc = (KB + 7) / 8, r32 = lane & 31;
 
-// One pass over 16 weight rows' K for NT tiles of 16 tokens from row r0; the waves take units
-// of 256 k in turn and join their sums in LDS in wave order.
-template <int NT>
-__device__ __forceinline__ void stream8_tiles(const ProductArgs& p, int g, int r0, int re, int n0, f32x4_t* red) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
-    const int KB = p.K / 32;
-    const int64_t n = (int64_t)g * p.N + min(n0 + col, p.N - 1);                     // rows past N: any valid row
-    const uint8_t* wrow = p.w + n * (p.K / 2);
-    const uint8_t* srow = p.w_s + n * KB;
-    const uint8_t* a = static_cast<const uint8_t*>(p.a);
-    f32x4_t acc[NT];
+    // This workgroup's tiles: workgroup b runs on XCD b % 8, each XCD takes a contiguous range.
+    int* table = reinterpret_cast<int*>(smem + (ALIGNED ? k8OffTable : 0));
+    const int all = tile_table(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
+    const int end = min(((int)blockIdx.x & 7) * per + per, all);
+    int mine = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+    if (mine >= end) return;
+    Tile t = table_tile(p, table, mine, NT);
+    if (!ALIGNED) __syncthreads();                       // the table's place is a stage's
+
+    // ---- loads: rows one chunk (256 k) ahead of the multiplication, half a chunk a slot; the
+    // weight and both operands' scales two chunks ahead.  Load q of wave w fills rows 8 (4 w + q)
+    // .. +8 of a slot (a full 128-byte line each), lane i row i / 8, slot i % 8, which holds unit
+    // (i & 7) ^ (i >> 3) ^ (q & 1) (swz8).  Scales: waves 0-3 the weight's rows 64 w .. +64, waves
+    // 4-7 the rows'.  Rows and outputs past the tile's end: any valid row (their results are not
+    // stored).
+    // (Lane offsets are formed at each load: kept, they would not leave the registers for the
+    // accumulators and operands.)
+    const uint8_t *abase, *wbase, *sbase;
+    int amax, wmax, smax;                                // last rows of the operands' parts
+    const int cu = (lane & 7) ^ (lane >> 3), lrow = wave * 32 + (lane >> 3), srow = (wave & 3) * 64;
+    const int sdst = k8OffS + (wave < 4 ? 0 : kScales);
+    Tile wt;                                             // the tile of the next weight loads
+    auto rows_from = [&](const Tile& n) {
+        abase = static_cast<const uint8_t*>(p.a) + (int64_t)n.rb * p.K;
+        amax = n.re - 1 - n.rb;
+    };
+    auto weight_from = [&](const Tile& n) {
+        wt = n;
+        const int n0 = n.nt * kTN;
+        const int64_t w0 = (int64_t)n.g * p.N + n0;
+        wbase = p.w + w0 * (p.K / 2);
+        wmax = p.N - 1 - n0;
+        sbase = wave < 4 ? p.w_s + w0 * KB : p.a_s + (int64_t)n.rb * KB;
+        smax = wave < 4 ? wmax : n.re - 1 - n.rb;
+    };
+    // the wave's part q of the rows' next half chunk (k 128 s ..)
+    auto issue_rows = [&](int s, int q) {
+        const uint32_t off = min(lrow + 8 * q, amax) * (uint32_t)p.K + (cu ^ (q & 1)) * 16;
+        const uint8_t* ab = abase + (int64_t)s * 128;
+        uint8_t* ad = smem + (s & 1) * k8Part + (wave * 4 + q) * 1024;
+        if (s * 4 + 4 <= KB) load_lds<16>(ab, off, ad);
+        else load_lds<16>(within(s * 128 + (cu ^ (q & 1)) * 16 < p.K, ab + off), ad);
+    };
+    auto issue_weight = [&](int c, int slot, int q) {
+        const uint32_t off = min(lrow + 8 * q, wmax) * (uint32_t)(p.K / 2) + (cu ^ (q & 1)) * 16;
+        const uint8_t* wb = wbase + (int64_t)c * 128;
+        uint8_t* wd = smem + k8OffW + slot * k8Part + (wave * 4 + q) * 1024;
+        if (c * 8 + 8 <= KB) load_lds<16>(wb, off, wd);
+        else load_lds<16>(within(c * 8 + (cu ^ (q & 1)) < KB, wb + off), wd);
+    };
+    int spair = 0;                                       // slot of the next scales
+    auto issue_scales = [&](int c) {                     // ALIGNED: at even chunks this one's and the next's
+        const uint8_t* sb = sbase + (int64_t)c * 8;
+        if (ALIGNED) {
+            if (c & 1) return;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int u = wave; u * 8 < KB; u += kSWaves) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int k0 = (u * 8 + s * 4) * 32, kb = u * 8 + s * 4 + lg;            // the step's first k, this lane's block
-            const bool kv = kb < KB;
-            u32x4_t wc = {0u, 0u, 0u, 0u};
-            uint32_t ws = 0u;
-            if (kv) {
-                wc = *reinterpret_cast<const u32x4_t*>(wrow + (int64_t)kb * 16);
-                ws = srow[kb];
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t off = min(srow + q * 16 + (lane >> 2), smax) * (uint32_t)KB + (lane & 3) * 4;
+                uint8_t* sd = smem + spair * kSlotS + sdst + srow * 16 + q * 256;
+                if (c * 8 + 16 <= KB) load_lds<4>(sb, off, sd);
+                else load_lds<4>(within(c * 8 + (lane & 3) * 4 < KB, sb + off), sd);
             }
+        } else {
+            const uint32_t off = min(srow + lane, smax) * (uint32_t)KB;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int64_t r = r0 + 16 * t + col;
-                const int ka = k0 + 16 * lg;
-                u32x4_t lo = {0u, 0u, 0u, 0u}, hi = {0u, 0u, 0u, 0u};
-                uint32_t as = 0u;
-                if (r < re) {
-                    if (ka < p.K) lo = *reinterpret_cast<const u32x4_t*>(a + r * p.K + ka);
-                    if (ka + 64 < p.K) hi = *reinterpret_cast<const u32x4_t*>(a + r * p.K + ka + 64);
-                    if (kv) as = p.a_s[r * KB + kb];
-                }
-                acc[t] = mfma_w4a8_16(wc, ws, lo, hi, as, acc[t]);
+            for (int i = 0; i < 8; ++i) {
+                uint8_t* sd = smem + spair * kSlotS + sdst + i * 1024 + srow * 4;
+                if (c * 8 + 8 <= KB) load_lds<1>(sb + i, off, sd);
+                else load_lds<1>(within(c * 8 + i < KB, sb + i + off), sd);
             }
         }
+        spair ^= 1;
+    };
+    // positions of the next loads: the rows' half chunk, the weight's chunk and its slot
+    int rs = 0, rnext = mine, wc = 0, wslot = 0, wnext = mine;
+    bool rmore = true, wmore = true;
+    auto advance_rows = [&]() {
+        if (++rs < 2 * nc) return;
+        rs = 0;
+        rnext += stride;
+        rmore = ALIGNED && rnext < end;
+        if (rmore) rows_from(wt);                        // the weight's loads have just come to this tile
+    };
+    auto advance_weight = [&]() {
+        wslot ^= 1;
+        if (++wc < nc) return;
+        wc = 0;
+        wnext += stride;
+        wmore = ALIGNED && wnext < end;
+        if (wmore) weight_from(table_tile(p, table, wnext, NT));
+    };
+
+    // ---- the multiplication: a half chunk is two groups of 64 k ----
+    f32x16_t acc[4][2];
+    u32x4_t wv[4], av[2][2][2];                          // operands; the rows' by parity of the group
+    uint32_t ws[4], as[2], wsn[4], asn[2];               // a chunk's scales, four groups'; the next chunk's
+    // of group m of half chunk `half`, the chunk's weight in `slot`
+    auto weights = [&](int half, int slot, int m, int j) {
+        wv[j] = *reinterpret_cast<const u32x4_t*>(smem + k8OffW + slot * k8Part +
+                                                  swz8(wn * 128 + j * 32 + r32, 4 * half + 2 * m + h));
+    };
+    auto tokens = [&](int half, auto m_c) {
+        constexpr int m = decltype(m_c)::value;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                av[m][i][q] = *reinterpret_cast<const u32x4_t*>(
+                    smem + half * k8Part + swz8(wm * 64 + i * 32 + r32, 4 * m + 2 * q + h));
+    };
+    // blocks h, 2 + h, 4 + h, 6 + h of row r's eight
+    auto row_scales = [&](const uint8_t* S, int r) {
+        if (ALIGNED) {
+            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(S + r * 16);
+            return __builtin_amdgcn_perm(v.y, v.x, h ? 0x07050301u : 0x06040200u);
+        }
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v |= *reinterpret_cast<const uint32_t*>(S + (2 * i + h) * 1024 + r * 4) << (8 * i);
+        return v;
+    };
+    int rpair = 1;                                       // slot of the scales being read
+    auto scales = [&](int c) {                           // of chunk c of its tile
+        if (!ALIGNED || !(c & 1)) rpair ^= 1;
+        const uint8_t* S = smem + k8OffS + rpair * kSlotS + (ALIGNED ? (c & 1) * 8 : 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wsn[j] = row_scales(S, wn * 128 + j * 32 + r32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) asn[i] = row_scales(S + kScales, wm * 64 + i * 32 + r32);
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ws[j] = wsn[j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) as[i] = asn[i];
+    };
+    auto mfmas = [&](auto half_c, auto m_c, int j, int nv) {
+        constexpr int half = decltype(half_c)::value, m = decltype(m_c)::value;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (i < nv)
+                acc[j][i] = mfma_w4a8_32<2 * half + m>(wv[j], ws[j], av[m][i][0], av[m][i][1], as[i], acc[j][i]);
+    };
+
+    // A tile's chunks.  A group's tokens are read before the MFMAs of the group before it, each
+    // weight operand after the last MFMA on the one before it, three operands ahead of its own
+    // MFMAs, so that the matrix cores do not wait for LDS.  The barrier stands before a half
+    // chunk's last MFMAs, where its slot has been read and the half chunk after the next may take
+    // it.  Loads return in order: at a chunk's middle the rows' next half must have landed and the
+    // weight loads issued after them (always the last four) may be under way; at its end everything.
+    constexpr std::integral_constant<int, 0> c0{};
+    constexpr std::integral_constant<int, 1> c1{};
+    int slot = 0;
+    bool wflight = false;                                // weight loads were issued last
+    auto stages = [&](int nv) {                          // nv: 32-row blocks of this wave with rows
+        for (int c = 0; c < nc; ++c) {
+            tokens(0, c1);
+            keep_order();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mfmas(c0, c0, j, nv);
+                weights(0, slot, 1, j);
+                keep_order();
+            }
+            if (wflight) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            tokens(1, c0);
+            keep_order();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mfmas(c0, c1, j, nv);
+                weights(1, slot, 0, j);
+                keep_order();
+                if (rmore) issue_rows(rs, j);
+                keep_order();
+            }
+            if (rmore) advance_rows();
+
+            tokens(1, c1);
+            keep_order();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mfmas(c1, c0, j, nv);
+                weights(1, slot, 1, j);
+                keep_order();
+            }
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            tokens(0, c0);
+            scales(c + 1 < nc ? c + 1 : 0);
+            keep_order();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mfmas(c1, c1, j, nv);
+                weights(0, slot ^ 1, 0, j);
+                keep_order();
+                if (rmore) issue_rows(rs, j);
+                keep_order();
+            }
+            wflight = wmore;
+            if (wmore) {
+                issue_scales(wc);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) issue_weight(wc, wslot, q);
+            }
+            if (rmore) advance_rows();
+            if (wmore) advance_weight();
+            take_scales();
+            slot ^= 1;
+        }
+    };
+
+    rows_from(t);
+    weight_from(t);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (rmore) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) issue_rows(rs, q);
+            advance_rows();
+        }
+        if (wmore) {
+            issue_scales(wc);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) issue_weight(wc, wslot, q);
+            advance_weight();
+        }
     }
-    __syncthreads();                                            // red's previous readers are done
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    tokens(0, c0);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) red[(wave * NT + t) * 64 + lane] = acc[t];
-    __syncthreads();
-    for (int x = threadIdx.x; x < NT * 64; x += 64 * kSWaves) {
-        f32x4_t s = red[x];
+    for (int j = 0; j < 4; ++j) weights(0, 0, 0, j);
+    scales(0);
+    take_scales();
+    for (;;) {
 #pragma unroll
-        for (int w = 1; w < kSWaves; ++w) s += red[w * NT * 64 + x];
-        const int l = x & 63, r = r0 + 16 * (x >> 6) + (l & 15), o = n0 + 4 * (l >> 4);
-        if (r < re) store4(p.out, p.out_dtype, r * p.os + o, s, p.N - o);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
+        const bool cols = t.nt * kTN + wn * 128 < p.N;
+        const int nvi = cols ? max(0, min(2, (t.re - t.rb - wm * 64 + 31) >> 5)) : 0;    // 32-row blocks with rows
+        stages(nvi);
+        if (!ALIGNED) __syncthreads();                   // staged in the stages' place
+        uint8_t* stage = smem + (ALIGNED ? k8OffStage : 0) + wave * kWaveStage / 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= nvi) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                wave_store_halves(p, stage, t, wm * 64 + i * 32, wn * 128 + j * 32, p.N, acc[j][i]);
+        }
+        mine += stride;
+        if (!ALIGNED || mine >= end) break;
+        t = table_tile(p, table, mine, NT);
     }
 }
 
-__global__ __launch_bounds__(64 * kSWaves) void product8_stream_kernel(ProductArgs p, int by_rank) {
-    __shared__ f32x4_t red[kSWaves * 4 * 64];
-    const int g = by_rank ? nth_group(p, blockIdx.y) : (int)blockIdx.y;
-    if (g < 0) return;
-    int rb, re;
-    group_rows(p, g, rb, re);
-    for (int r0 = rb; r0 < re;) {
-        const int left = re - r0;
-        if (left > 32) { stream8_tiles<4>(p, g, r0, re, blockIdx.x * 16, red); r0 += 64; }
-        else if (left > 16) { stream8_tiles<2>(p, g, r0, re, blockIdx.x * 16, red); r0 += 32; }
-        else { stream8_tiles<1>(p, g, r0, re, blockIdx.x * 16, red); r0 += 16; }
-    }
-}
-
-hipError_t launch_product8(const ProductArgs& p, int cus, hipStream_t s) {
-    const int groups = min(p.G, p.M);                           // at most so many hold rows
-    hipLaunchKernelGGL(product8_stream_kernel, dim3((p.N + 15) / 16, groups), dim3(64 * kSWaves), 0, s, p,
-                       p.M < p.G ? 1 : 0);
-    return hipGetLastError();
+hipError_t launch_product8_tiles(const ProductArgs& p, int cus, hipStream_t s) {
+    const bool aligned =
+        p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
+    const int64_t tiles = tile_grid(p, (p.N + kTN - 1) / kTN);
+    // one workgroup a CU, each for several tiles, or (tiles: a multiple of 8) one a tile
+    return aligned ? launch_tiles<w4a8_tile_kernel<true>, w4a8_lds(true)>(p, min(tiles, (int64_t)max(cus / 8 * 8, 8)), s)
+                   : launch_tiles<w4a8_tile_kernel<false>, w4a8_lds(false)>(p, tiles, s);
 }
 
 }  // namespace moe

@@ -71,6 +71,19 @@ __device__ __forceinline__ f32x4_t mfma_mx16(const u32x4_t& a, uint32_t as, cons
                                                             (int)bs);
 }
 
+// MXFP8 rows as the column operand.  Of a step's k (128; 64 of the 32 x 32 instruction) a lane
+// group g holds the 32 codes of block g as the FP4 operand, but as the FP8 operand the 16 from
+// 16 g and the 16 from half the step + 16 g; either gives the scale of block g (checked on the
+// device).
+__device__ __forceinline__ i32x8_t mx8_operand(const u32x4_t& lo, const u32x4_t& hi) {
+    return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+__device__ __forceinline__ f32x4_t mfma_w4a8_16(const u32x4_t& w, uint32_t ws, const u32x4_t& lo, const u32x4_t& hi,
+                                                uint32_t as, const f32x4_t& c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(w), mx8_operand(lo, hi), c, 4, 0, 0, (int)ws, 0,
+                                                            (int)as);
+}
+
 __device__ __forceinline__ f32x4_t mfma_bf16_16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
                                                    c, 0, 0, 0);
