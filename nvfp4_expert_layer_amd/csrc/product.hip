@@ -1,4 +1,4 @@
-// MXFP4 products over rows sorted by group, few rows a group (gfx950):
+// Products with MXFP4 weights over rows sorted by group, few rows a group (gfx950):
 //   forward   out[r][n]   = sum_k a[r][k] w[g(r)][n][k]
 //   backward  drows[r][k] = sum_n dout[r][n] w[g(r)][n][k]
 // With few rows the weight's bytes are the whole cost: each group's weight is read once
@@ -6,9 +6,9 @@
 // order; a workgroup's waves split the reduction and join their sums in LDS in wave
 // order, so nothing depends on timing.
 //
-//   product_resident_kernel  forward, K up to 4096 (W4A4: 8192).  512 rows over 160
-//       experts of 2048 x 4096: W4A16 131 us, 5.4 TB/s, W4A4 122 us, 5.8 TB/s (a large
-//       copy: 4.95); one row of 2048 x 4096: 4.9 us.  The form below it, which loads tokens
+//   product_resident_kernel  forward, K up to 4096 (MXFP4, MXFP8 rows: 8192).  512 rows over
+//       160 experts of 2048 x 4096: W4A16 131 us, 5.4 TB/s, W4A4 122 us, 5.8 TB/s, W4A8 125 us
+//       (a large copy: 4.95); one row of 2048 x 4096: 4.9 us.  The form below it, which loads tokens
 //       again for each weight tile, took 216 us for the 512 rows.
 //   product_stream_kernel    forward, longer K.
 //   product_grad_stream_kernel  512 rows over 160 experts: 236 us, 3.0 TB/s (268 before
@@ -22,6 +22,7 @@
 // four consecutive outputs of one token.
 //   W4A4: v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 codes (16 bytes) and one E8M0
 //     scale a lane: one 32-element block as it lies in memory, no decoding.
+//   W4A8: the same instruction with FP8 columns (two pieces of 16 k a lane).
 //   W4A16: 16 bytes of codes are four operands of v_mfma_f32_16x16x32_bf16;
 //     v_cvt_scalef32_pk_bf16_fp4 decodes a pair with its block scale, exactly.
 #include "device_common.h"
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(64 * kSWaves) void product_stream_kernel(ProductArg
 }
 
 // ---------------------------------------------------------------------------
-// forward, K up to 4096 (W4A4: 8192): eight waves split K into contiguous parts of KS steps (128 k),
+// forward, K up to 4096 (MXFP4, MXFP8 rows: 8192): eight waves split K into contiguous parts of KS steps (128 k),
 // each keeps its part of the tokens in registers and walks the workgroup's weight
 // tiles (16 rows) with the codes of the next two in flight, so that only weights
 // stream; one barrier a tile joins the waves' sums.
@@ -459,7 +460,17 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // M is the buffer's: where few of its rows are kept or one group holds many of them the rule
 // can pick the slower kernel (W4A16, 160 experts of 2048 x 4096: 3500 rows 198 / 236 spread
 // evenly, 572 / 324 after a Zipf law; 40 of 320 experts, an eighth of 2048 rows kept, 47 / 71).
+//
+// MXFP8 rows: the tile kernel's stages are half as deep, so one tile alone takes longer (one
+// of K = 4096: 40 us) and streaming wins for more rows.  Streamed / tiled: 160 groups of 2048 x
+// 4096 160 / 222 at 32 rows a group, 275 / 236 at 48; 64 groups 60 / 90 and 102 / 97; with the
+// tiles of one row block on a quarter of the card (8 groups) 37 / 43 at 96, 48 / 43 at 128; on a
+// twelfth or less (one group of 4096 x 4096) 45 / 48 at 192, 59 / 49 at 256.
 static bool streamed(const ProductArgs& p, int cus) {
+    if (p.a8) {
+        const int64_t one = (int64_t)p.G * ((p.N + 255) / 256);
+        return p.M <= (int64_t)p.G * (one * 12 <= cus ? 200 : (one * 4 <= cus ? 110 : 40));
+    }
     const int rows = p.a_s ? 20 : 24;
     const int64_t most = p.a_s ? 8 : 12, tiles = (int64_t)p.G * ((p.N + 255) / 256);
     const int64_t idle = min(most, cus / (4 * tiles));

@@ -1,0 +1,25 @@
+"""Which kernels a product of MXFP8 rows takes, on a card of 256 CUs (CPU): the launches' own rule."""
+import ctypes
+
+import pytest
+
+import nvfp4_expert_layer_amd as nv
+
+
+def streams(M, N, K, G, cus=256):
+    f = nv.lib().moe_internal_product_streams
+    f.argtypes = [ctypes.c_int] * 4 + [ctypes.c_int64] + [ctypes.c_int] * 3
+    f.restype = ctypes.c_int
+    return bool(f(M, N, K, G, K, 2, 0, cus))
+
+
+@pytest.mark.parametrize("G,N,K,lower,upper", [(160, 2048, 4096, 32, 48), (64, 2048, 4096, 32, 48), (8, 2048, 4096, 96, 128),
+                                               (16, 1024, 2048, 96, 128), (1, 4096, 4096, 192, 256), (1, 256, 4096, 192, 256),
+                                               (1, 16384, 4096, 96, 128)])
+def test_measured_crossings(G, N, K, lower, upper):
+    """Streamed at the lower count of rows a group, tiled at the upper."""
+    assert streams(lower * G, N, K, G) and not streams(upper * G, N, K, G)
+
+
+def test_extremes():
+    assert streams(1, 1, 32, 1) and streams(1, 65536, 65536, 1024) and not streams(1 << 27, 65536, 65536, 1024)
