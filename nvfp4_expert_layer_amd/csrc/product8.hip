@@ -17,13 +17,12 @@ namespace moe {
 
 constexpr int k8Part = 256 * 128;                          // a slot: 128 k of the rows, 256 k of the weight
 constexpr int k8OffW = 2 * k8Part, k8OffS = 4 * k8Part;    // rows [2] | weight [2] | scales [2] | ...
-// Scales of 512 k of both operands, or (rows of scales that are not aligned to dwords) of 256 k,
-// each byte in a dword of its own.
-constexpr int k8Pair = 2 * scale_bytes(true, 16), k8Bytes = 2 * scale_bytes(false, 8);
-// ... | waves' staging [8] | table.  Without aligned scales the stages take all 160 KB: one
-// tile a workgroup, staged and looked up in the stages' place.
-constexpr int k8OffStage = k8OffS + 2 * k8Pair, k8OffTable = k8OffStage + kTWaves * kWaveStage / 2;
-constexpr int w4a8_lds(bool aligned) { return aligned ? k8OffTable + kTable : k8OffS + 2 * k8Bytes; }
+// Scales of both operands, 16 bytes a row: of 512 k, or (rows of scales that are not aligned to
+// dwords) of 256 k, the aligned dwords that hold them.
+constexpr int k8Scales = scale_bytes(true, 16);
+// ... | waves' staging [8] | table
+constexpr int k8OffStage = k8OffS + 4 * k8Scales, k8OffTable = k8OffStage + kTWaves * kWaveStage / 2;
+constexpr int k8Lds = k8OffTable + kTable;
 
 template <int OPSEL>
 __device__ __forceinline__ f32x16_t mfma_w4a8_32(const u32x4_t& w, uint32_t ws, const u32x4_t& lo, const u32x4_t& hi,
@@ -51,23 +50,23 @@ __device__ __forceinline__ Tile band_tile(const ProductArgs& p, const int* table
 
 // A workgroup takes tiles one after another: while a tile's last stages are multiplied the next
 // tile's first ones are loaded, and its outputs leave while those land.
-// ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales).
+// ALIGNED: scale rows can be read in dwords (K % 128 == 0, 4-byte aligned scales), two chunks at a
+// time.  Otherwise each chunk's eight bytes come with the dwords that hold them and are shifted
+// into place (12004 rows over 24 experts of 1000 x 2080: 47 us byte by byte, 41 so).
 template <bool ALIGNED>
 __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
-    constexpr int kSlotS = ALIGNED ? k8Pair : k8Bytes, kScales = kSlotS / 2;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int wm = wave >> 1, wn = wave & 1;             // rows 64 wm .. +64, outputs 128 wn .. +128
     const int NT = (p.N + kTN - 1) / kTN, KB = p.K / 32, nc = (KB + 7) / 8, r32 = lane & 31;
 
     // This workgroup's tiles: workgroup b runs on XCD b % 8, each XCD takes a contiguous range.
-    int* table = reinterpret_cast<int*>(smem + (ALIGNED ? k8OffTable : 0));
+    int* table = reinterpret_cast<int*>(smem + k8OffTable);
     const int all = tile_table(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
     const int end = min(((int)blockIdx.x & 7) * per + per, all);
     int mine = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
     if (mine >= end) return;
     Tile t = band_tile(p, table, mine, NT);
-    if (!ALIGNED) __syncthreads();                       // the table's place is a stage's
 
     // ---- loads: rows one chunk (256 k) ahead of the multiplication, half a chunk a slot; the
     // weight and both operands' scales two chunks ahead.  Load q of wave w fills rows 8 (4 w + q)
@@ -80,11 +79,18 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
     const uint8_t *abase, *wbase, *sbase;
     int amax, wmax, smax;                                // last rows of the operands' parts
     const int cu = (lane & 7) ^ (lane >> 3), lrow = wave * 32 + (lane >> 3), srow = (wave & 3) * 64;
-    const int sdst = k8OffS + (wave < 4 ? 0 : kScales);
+    const int sdst = k8OffS + (wave < 4 ? 0 : k8Scales);
     Tile wt;                                             // the tile of the next weight loads
+    uint32_t wshift = 0, ashift = 0;                     // !ALIGNED: the lane's scale rows' first byte in a dword
     auto rows_from = [&](const Tile& n) {
         abase = static_cast<const uint8_t*>(p.a) + (int64_t)n.rb * p.K;
         amax = n.re - 1 - n.rb;
+        if (!ALIGNED) {                                  // (the rows' loads are one chunk ahead, as are the scales read)
+            const uintptr_t w = reinterpret_cast<uintptr_t>(p.w_s) + ((int64_t)n.g * p.N + n.nt * kTN) * KB;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(p.a_s) + (int64_t)n.rb * KB;
+            wshift = ((uint32_t)w + r32 * KB) & 3;
+            ashift = ((uint32_t)a + r32 * KB) & 3;
+        }
     };
     auto weight_from = [&](const Tile& n) {
         wt = n;
@@ -112,24 +118,17 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
     };
     int spair = 0;                                       // slot of the next scales
     auto issue_scales = [&](int c) {                     // ALIGNED: at even chunks this one's and the next's
-        const uint8_t* sb = sbase + (int64_t)c * 8;
-        if (ALIGNED) {
-            if (c & 1) return;
+        if (ALIGNED && (c & 1)) return;
+        const uint32_t mis = ALIGNED ? 0 : (uint32_t)reinterpret_cast<uintptr_t>(sbase) & 3;
+        const uint8_t* sb = sbase - mis + (int64_t)c * 8;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t off = min(srow + q * 16 + (lane >> 2), smax) * (uint32_t)KB + (lane & 3) * 4;
-                uint8_t* sd = smem + spair * kSlotS + sdst + srow * 16 + q * 256;
-                if (c * 8 + 16 <= KB) load_lds<4>(sb, off, sd);
-                else load_lds<4>(within(c * 8 + (lane & 3) * 4 < KB, sb + off), sd);
-            }
-        } else {
-            const uint32_t off = min(srow + lane, smax) * (uint32_t)KB;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint8_t* sd = smem + spair * kSlotS + sdst + i * 1024 + srow * 4;
-                if (c * 8 + 8 <= KB) load_lds<1>(sb + i, off, sd);
-                else load_lds<1>(within(c * 8 + i < KB, sb + i + off), sd);
-            }
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t row = min(srow + q * 16 + (lane >> 2), smax) * (uint32_t)KB + mis;
+            const uint32_t off = (row & ~3u) + (lane & 3) * 4;
+            uint8_t* sd = smem + spair * 2 * k8Scales + sdst + srow * 16 + q * 256;
+            if (!ALIGNED) load_lds<4>(within(c * 8 + off < (smax + 1) * (uint32_t)KB + mis, sb + off), sd);
+            else if (c * 8 + 16 <= KB) load_lds<4>(sb, off, sd);
+            else load_lds<4>(within(c * 8 + (lane & 3) * 4 < KB, sb + off), sd);
         }
         spair ^= 1;
     };
@@ -140,7 +139,7 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
         if (++rs < 2 * nc) return;
         rs = 0;
         rnext += stride;
-        rmore = ALIGNED && rnext < end;
+        rmore = rnext < end;
         if (rmore) rows_from(wt);                        // the weight's loads have just come to this tile
     };
     auto advance_weight = [&]() {
@@ -148,7 +147,7 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
         if (++wc < nc) return;
         wc = 0;
         wnext += stride;
-        wmore = ALIGNED && wnext < end;
+        wmore = wnext < end;
         if (wmore) weight_from(band_tile(p, table, wnext, NT));
     };
 
@@ -171,24 +170,27 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
                     smem + half * k8Part + swz8(wm * 64 + i * 32 + r32, 4 * m + 2 * q + h));
     };
     // blocks h, 2 + h, 4 + h, 6 + h of row r's eight
-    auto row_scales = [&](const uint8_t* S, int r) {
+    auto row_scales = [&](const uint8_t* S, int r, uint32_t shift, int left) {
+        const uint32_t pick = h ? 0x07050301u : 0x06040200u;
         if (ALIGNED) {
             const u32x2_t v = *reinterpret_cast<const u32x2_t*>(S + r * 16);
-            return __builtin_amdgcn_perm(v.y, v.x, h ? 0x07050301u : 0x06040200u);
+            return __builtin_amdgcn_perm(v.y, v.x, pick);
         }
-        uint32_t v = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v |= *reinterpret_cast<const uint32_t*>(S + (2 * i + h) * 1024 + r * 4) << (8 * i);
-        return v;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(S + r * 16);
+        uint32_t lo = __builtin_amdgcn_alignbyte(v.y, v.x, shift), hi = __builtin_amdgcn_alignbyte(v.z, v.y, shift);
+        if (left < 8) {                                  // past K come another row's: its NaN times a 0 would stay
+            lo &= left >= 4 ? ~0u : (1u << (8 * left)) - 1;
+            hi &= left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1;
+        }
+        return __builtin_amdgcn_perm(hi, lo, pick);
     };
     int rpair = 1;                                       // slot of the scales being read
-    auto scales = [&](int c) {                           // of chunk c of its tile
-        if (!ALIGNED || !(c & 1)) rpair ^= 1;
-        const uint8_t* S = smem + k8OffS + rpair * kSlotS + (ALIGNED ? (c & 1) * 8 : 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) wsn[j] = row_scales(S, wn * 128 + j * 32 + r32);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) asn[i] = row_scales(S + kScales, wm * 64 + i * 32 + r32);
+    auto scales = [&](int c, int j) {                    // of chunk c of its tile: part j of 4
+        if (j == 0 && (!ALIGNED || !(c & 1))) rpair ^= 1;
+        const uint8_t* S = smem + k8OffS + rpair * 2 * k8Scales + (ALIGNED ? (c & 1) * 8 : 0);
+        const int left = KB - c * 8;
+        wsn[j] = row_scales(S, wn * 128 + j * 32 + r32, wshift, left);
+        if (j < 2) asn[j] = row_scales(S + k8Scales, wm * 64 + j * 32 + r32, ashift, left);
     };
     auto take_scales = [&]() {
 #pragma unroll
@@ -248,12 +250,12 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
             }
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             tokens(0, c0);
-            scales(c + 1 < nc ? c + 1 : 0);
             keep_order();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 mfmas(c1, c1, j, nv);
                 weights(0, slot ^ 1, 0, j);
+                scales(c + 1 < nc ? c + 1 : 0, j);
                 keep_order();
                 if (rmore) issue_rows(rs, j);
                 keep_order();
@@ -290,8 +292,10 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     tokens(0, c0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) weights(0, 0, 0, j);
-    scales(0);
+    for (int j = 0; j < 4; ++j) {
+        weights(0, 0, 0, j);
+        scales(0, j);
+    }
     take_scales();
     for (;;) {
 #pragma unroll
@@ -303,8 +307,7 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
         const bool cols = t.nt * kTN + wn * 128 < p.N;
         const int nvi = cols ? max(0, min(2, (t.re - t.rb - wm * 64 + 31) >> 5)) : 0;    // 32-row blocks with rows
         stages(nvi);
-        if (!ALIGNED) __syncthreads();                   // staged in the stages' place
-        uint8_t* stage = smem + (ALIGNED ? k8OffStage : 0) + wave * kWaveStage / 2;
+        uint8_t* stage = smem + k8OffStage + wave * kWaveStage / 2;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (i >= nvi) break;
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
                 wave_store_halves(p, stage, t, wm * 64 + i * 32, wn * 128 + j * 32, p.N, acc[j][i]);
         }
         mine += stride;
-        if (!ALIGNED || mine >= end) break;
+        if (mine >= end) break;
         t = band_tile(p, table, mine, NT);
     }
 }
@@ -321,10 +324,9 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
 hipError_t launch_product8_tiles(const ProductArgs& p, int cus, hipStream_t s) {
     const bool aligned =
         p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
-    const int64_t tiles = tile_grid(p, (p.N + kTN - 1) / kTN);
-    // one workgroup a CU, each for several tiles, or (tiles: a multiple of 8) one a tile
-    return aligned ? launch_tiles<w4a8_tile_kernel<true>, w4a8_lds(true)>(p, min(tiles, (int64_t)max(cus / 8 * 8, 8)), s)
-                   : launch_tiles<w4a8_tile_kernel<false>, w4a8_lds(false)>(p, tiles, s);
+    const int64_t grid = min(tile_grid(p, (p.N + kTN - 1) / kTN), (int64_t)max(cus / 8 * 8, 8));   // one workgroup a CU
+    return aligned ? launch_tiles<w4a8_tile_kernel<true>, k8Lds>(p, grid, s)
+                   : launch_tiles<w4a8_tile_kernel<false>, k8Lds>(p, grid, s);
 }
 
 }  // namespace moe
