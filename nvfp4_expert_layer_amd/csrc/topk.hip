@@ -1,11 +1,21 @@
 // Route (gfx950): a token's experts and weights from its router logits, and the logits'
 // gradient from the weights'.
 //
-// A wave takes a token.  With LG = 64 / groups lanes (a power of two) to a group, lane l
-// holds experts gs (l / LG) + LG j + l % LG of groups of gs experts: a group's highest keys
-// meet in LG lanes, and every round of the choice is one maximum over the wave.  Keys are
-// compared in fp64: their order is then that of the definition (two different fp32 logits
-// give scores whose fp32 roundings may tie or swap).
+// The choice.  A wave takes a token.  With LG = 64 / groups lanes (a power of two) to a group,
+// lane l holds experts gs (l / LG) + LG j + l % LG of groups of gs experts: a group's highest
+// keys meet in LG lanes, and every round of the choice is one maximum over the wave.  Keys are
+// 32-bit integers that order as floats:
+//   without bias and groups, the logits: exact, equal ones go to the lowest id;
+//   else fp32 scores (hardware exp2 and reciprocal) plus bias.  Each is within
+//     2^-24 (C smax + |key|) of the exact key, with C = 6, smax = 1 for a sigmoid (argument,
+//     exp2, sum, reciprocal; s (1 - s) |l| < 0.23) and C = 40, smax = the highest score for a
+//     softmax of at most 1024 terms.  The choice stands if every two neighbours among the k + 1
+//     highest keys, and the last group in and the first group out, are further apart than their
+//     bounds; else the token is done again in fp64, whose order is the definition's (about one
+//     in a thousand).
+// Weights are fp64 of the chosen logits alone, rounded once.
+//
+// Bound by issue: of T=16384 over 320 experts in 8 groups MEASURED
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -23,60 +33,120 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t el) {
     return sane(to_f32<DT>(static_cast<const typename Elem<DT>::type*>(p)[el]));
 }
 
-__device__ __forceinline__ double wave_max_f64(double v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-    return v;
+// ---------------------------------------------------------------------------
+// Reductions over the wave through DPP (rows of 16 by shifts, then rows into rows); the result
+// is the same in every lane.
+// ---------------------------------------------------------------------------
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t none) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
+}
+// v combined with the lane that CTRL names, or with the neutral element.
+template <int CTRL, int ROWS, typename F>
+__device__ __forceinline__ uint32_t dpp_step(uint32_t v, uint32_t none, F f) { return f(v, dpp<CTRL, ROWS>(v, none)); }
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t none, F f) {
+    v = dpp_step<0x111, 0xF>(v, none, f);                         // row_shr 1, 2, 4, 8
+    v = dpp_step<0x112, 0xF>(v, none, f);
+    v = dpp_step<0x114, 0xF>(v, none, f);
+    v = dpp_step<0x118, 0xF>(v, none, f);
+    v = dpp_step<0x142, 0xA>(v, none, f);                         // row_bcast 15 into rows 1, 3
+    v = dpp_step<0x143, 0xC>(v, none, f);                         // row_bcast 31 into rows 2, 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+// Over the lanes of a group of LG (a power of two): lanes trade places within quads, then halves
+// of eight and rows of sixteen mirror each other, whose lanes agree by then.
+template <typename F>
+__device__ __forceinline__ void group_steps(int LG, F f) {
+    if (LG > 1) f([](uint32_t v) { return dpp<0xB1, 0xF>(v, v); });
+    if (LG > 2) f([](uint32_t v) { return dpp<0x4E, 0xF>(v, v); });
+    if (LG > 4) f([](uint32_t v) { return dpp<0x141, 0xF>(v, v); });
+    if (LG > 8) f([](uint32_t v) { return dpp<0x140, 0xF>(v, v); });
+    if (LG > 16) f([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 16, 64); });
+    if (LG > 32) f([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 32, 64); });
+}
+__device__ __forceinline__ float wave_total(float v) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t o = (uint64_t)dpp<CTRL, ROWS>((uint32_t)(u >> 32), 0u) << 32 | dpp<CTRL, ROWS>((uint32_t)u, 0u);
+    return v + __builtin_bit_cast(double, o);
+}
+__device__ __forceinline__ double wave_total(double v) {
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);
+    v = dpp_add<0x143, 0xC>(v);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// Integers that order as the floats do, -0 below +0; those below kKeys stand for no key (-Inf).
+constexpr uint32_t kKeys = 0x00800000u;
+__device__ __forceinline__ uint32_t order_bits(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t u) {
+    return __uint_as_float(u ^ ((uint32_t)~((int32_t)u >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ float wave_top(float v) { return order_value(wave_max_u32(order_bits(v))); }
+
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-template <int DT, int VPL>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int LG, int gs) {
-    const int lane = threadIdx.x & 63, group = lane / LG, within = lane & (LG - 1);
-    const int waves = blockDim.x >> 6;
-    const bool scored = a.bias || a.top_groups < a.groups;       // else keys order as the logits do
-    for (int64_t token = (int64_t)blockIdx.x * waves + (threadIdx.x >> 6); token < a.T; token += (int64_t)gridDim.x * waves) {
-    float l[VPL];
-    int e[VPL];
+enum RouteKind { kByLogit, kBySigmoid, kBySoftmax };              // what keys are made of
+
+// A lane's experts: ids first + j * step, of group `group` (idle lanes: bias -Inf).
+struct RouteLane {
+    int shift, gs, group, first, step;                           // lanes to a group: 1 << shift
+};
+
+// The choice in fp64, by the definition: the q-th expert's id to lane slot + q (-1 stays).
+template <int KIND, int VPL>
+__device__ __forceinline__ void choose64(const RouteArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
+                                         const RouteLane& o, int slot, int& id) {
+    const int lane = threadIdx.x & 63, LG = 1 << o.shift;
     float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        const int i = j * LG + within;
-        e[j] = group < a.groups && i < gs ? group * gs + i : -1;
-        l[j] = e[j] >= 0 ? load_logit<DT>(a.logits, token * a.ls + e[j]) : -INFINITY;
-        top = fmaxf(top, l[j]);
-    }
     double sum = 1.0;
-    if (!a.sigmoid && (scored || !a.renormalize)) {
-        top = wave_max_f32(top);
+    if (KIND == kBySoftmax) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) top = fmaxf(top, l[j]);
+        top = wave_top(top);
         sum = 0.0;
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
             if (l[j] > -INFINITY) sum += exp((double)l[j] - (double)top);
-        sum = wave_sum_f64(sum);
+        sum = wave_total(sum);
     }
     double key[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
         key[j] = (double)l[j];
-        if (scored && l[j] > -INFINITY) {
-            key[j] = a.sigmoid ? sigmoid64(l[j]) : exp((double)l[j] - (double)top) / sum;
-            if (a.bias) {
-                key[j] += (double)a.bias[e[j]];
-                if (!(key[j] > -INFINITY)) key[j] = -INFINITY;   // NaN
-            }
-        }
+        if (KIND != kByLogit && l[j] > -INFINITY)
+            key[j] = (KIND == kBySigmoid ? sigmoid64(l[j]) : exp((double)l[j] - (double)top) / sum) + (double)bias[j];
     }
-    if (a.top_groups < a.groups) {
+    if (KIND != kByLogit && a.top_groups < a.groups) {
         double b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             b2 = fmax(b2, fmin(b1, key[j]));
             b1 = fmax(b1, key[j]);
         }
-        for (int o = 1; o < LG; o <<= 1) {
-            const double c1 = __shfl_xor(b1, o, 64), c2 = __shfl_xor(b2, o, 64);
+        for (int i = 1; i < LG; i <<= 1) {
+            const double c1 = __shfl_xor(b1, i, 64), c2 = __shfl_xor(b2, i, 64);
             b2 = fmax(fmin(b1, c1), fmax(b2, c2));
             b1 = fmax(b1, c1);
         }
@@ -84,14 +154,14 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int LG, int gs)
         int ahead = 0;
         for (int g = 0; g < a.groups; ++g) {
             const double other = __shfl(b1, g * LG, 64);
-            ahead += other > b1 || (other == b1 && g < group) ? 1 : 0;
+            ahead += other > b1 || (other == b1 && g < o.group) ? 1 : 0;
         }
         if (ahead >= a.top_groups) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j) key[j] = -INFINITY;
         }
     }
-    int id = -1;                                                  // lane q: the q-th expert
+    if ((uint32_t)(lane - slot) < (uint32_t)a.k) id = -1;
     for (int q = 0; q < a.k; ++q) {
         double best = -INFINITY;
         int at = INT_MAX;
@@ -99,43 +169,196 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int LG, int gs)
         for (int j = 0; j < VPL; ++j)
             if (key[j] > best) {
                 best = key[j];
-                at = e[j];
+                at = o.first + j * o.step;
             }
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const double b = __shfl_xor(best, o, 64);
-            const int i = __shfl_xor(at, o, 64);
-            if (b > best || (b == best && i < at)) {
+        for (int i = 32; i > 0; i >>= 1) {
+            const double b = __shfl_xor(best, i, 64);
+            const int e = __shfl_xor(at, i, 64);
+            if (b > best || (b == best && e < at)) {
                 best = b;
-                at = i;
+                at = e;
             }
         }
         if (!(best > -INFINITY)) break;
-        if (lane == q) id = at;
+        if (lane == slot + q) id = at;
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
-            if (e[j] == at) key[j] = -INFINITY;
+            if (o.first + j * o.step == at) key[j] = -INFINITY;
     }
-    // weights: lane q's
-    const float mine = id >= 0 ? load_logit<DT>(a.logits, token * a.ls + id) : -INFINITY;
-    double s = 0.0;
-    if (a.sigmoid) {
-        if (id >= 0) s = sigmoid64(mine);
+}
+
+// The same from 32-bit keys whose low BITS bits name j, lower ones first; false: not certain.  EXACT
+// (16-bit logits, which leave these bits 0): every key as it is, so nothing is left open; equal
+// ones go by j, then by lane, which is by id where all lanes are one group.
+template <int KIND, int VPL, bool EXACT>
+__device__ __forceinline__ bool choose32(const RouteArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
+                                         const RouteLane& o, int slot, int& id) {
+    constexpr float U = 1.0f / (1 << 24);
+    constexpr int BITS = VPL <= 1 ? 0 : (VPL <= 2 ? 1 : (VPL <= 8 ? 3 : 5)), MASK = (1 << BITS) - 1;
+    constexpr float R = (2 * (1 << BITS) + 1.02f) * U;           // relative: the low bits, the bias's addition
+    const int lane = threadIdx.x & 63, LG = 1 << o.shift;
+    float key[VPL], base = 0.f;                                  // base: C smax 2^-24
+    if constexpr (KIND == kByLogit) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) key[j] = l[j] + 0.0f;      // -0 is +0
     } else {
-        if (a.renormalize) {
-            top = wave_max_f32(mine);
-            sum = 1.0;                                            // cancels
+        float smax = 1.0f;
+        if (KIND == kBySoftmax) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) top = fmaxf(top, l[j]);
+            top = wave_top(top);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                key[j] = l[j] > -INFINITY ? fast_exp(l[j] - top) : 0.f;
+                sum += key[j];
+            }
+            smax = __builtin_amdgcn_rcpf(wave_total(sum));
         }
-        if (id >= 0) s = exp((double)mine - (double)top) / sum;
+        base = (KIND == kBySigmoid ? 6.0f : 40.0f) * U * smax;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            key[j] = (KIND == kBySigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[j])) : key[j] * smax) + bias[j];
+            if (!(l[j] > -INFINITY)) key[j] = -INFINITY;
+        }
+        if (a.top_groups < a.groups) {
+            float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                b2 = fmaxf(b2, fminf(b1, key[j]));
+                b1 = fmaxf(b1, key[j]);
+            }
+            group_steps(LG, [&](auto swap) {
+                const float c1 = __uint_as_float(swap(__float_as_uint(b1))), c2 = __uint_as_float(swap(__float_as_uint(b2)));
+                b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
+                b1 = fmaxf(b1, c1);
+            });
+            const bool two = a.group_keys == 2 && b2 > -INFINITY, any = b1 > -INFINITY;
+            const float own = two ? b1 + b2 : b1;
+            // what the sum may be off by
+            const float off = !any ? 0.f : (two ? 2.f * base + (fabsf(b1) + fabsf(b2) + fabsf(own)) * U * 1.01f
+                                                : base + fabsf(b1) * U * 1.01f);
+            int ahead = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const float other =
+                    __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(own), g << o.shift));
+                ahead += other > own ? 1 : 0;                    // (equal ones in and out are not certain)
+            }
+            const bool live = o.group < a.groups, in = live && ahead < a.top_groups;
+            const float last_in = -wave_top(in ? -(own - off) : -INFINITY);
+            const float first_out = wave_top(live && !in ? own + off : -INFINITY);
+            if (!(last_in > first_out)) return false;
+            if (!in) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) key[j] = -INFINITY;
+            }
+        }
     }
-    if (a.renormalize) {
-        const double total = wave_sum_f64(s);
-        s = total > 0.0 ? s / total : 0.0;
+    uint32_t u[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) u[j] = (order_bits(key[j]) & ~(uint32_t)MASK) | (uint32_t)(VPL - 1 - j);
+    uint32_t got = 0, from = 0, after = 0;                       // lane slot + q: the q-th key and its lane
+    for (int q = 0; q <= a.k; ++q) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) m = m > u[j] ? m : u[j];
+        after = wave_max_u32(m);
+        if (after < kKeys || q == a.k) break;
+        const uint64_t who = __ballot(m == after);
+        if (!EXACT && (who & (who - 1))) return false;
+        const int w = __ffsll((unsigned long long)who) - 1;
+        if (lane == slot + q) {
+            got = after;
+            from = (uint32_t)w;
+        }
+        const bool mine = lane == w;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) u[j] = mine && u[j] == after ? 0u : u[j];
     }
-    if (lane < a.k) {
-        a.ids[token * a.k + lane] = id;
-        a.w[token * a.k + lane] = (float)((double)a.scale * s);
+    const int q = lane - slot;
+    const bool ours = (uint32_t)q < (uint32_t)a.k && got >= kKeys;
+    if (!EXACT) {
+        // every key further from the next than both may be off by
+        uint32_t next = (uint32_t)__shfl_down((int)got, 1, 64);
+        if (q == a.k - 1) next = after;
+        const float x = order_value(got), y = order_value(next);
+        const bool open = ours && next >= kKeys && !(x - y > 2.f * base + (fabsf(x) + fabsf(y)) * R + 1e-36f);
+        if (__ballot(open)) return false;
     }
+    if (ours) id = (int)(from >> o.shift) * o.gs + (VPL - 1 - (int)(got & MASK)) * LG + (int)(from & (LG - 1));
+    return true;
+}
+
+// A wave takes `batch` tokens one after another; their weights, a token's in a segment of 16 (k up
+// to 16) or 32 lanes, are then computed together.
+template <int DT, int VPL, int KIND>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int shift, int gs, int batch) {
+    const int lane = threadIdx.x & 63, LG = 1 << shift, group = lane >> shift, within = lane & (LG - 1);
+    const int waves = blockDim.x >> 6, seg = a.k <= 16 ? 16 : 32, q = lane & (seg - 1), own = lane >> (a.k <= 16 ? 4 : 5);
+    const RouteLane o{shift, gs, group, group * gs + within, LG};
+    const bool whole = !a.sigmoid && !a.renormalize;             // weights need every expert's score
+    const bool idle = group * gs >= a.E;
+    float bias[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        bias[j] = idle || j * LG + within >= gs ? -INFINITY : (KIND != kByLogit && a.bias ? a.bias[o.first + j * LG] : 0.f);
+        if (!(bias[j] > -INFINITY)) bias[j] = -INFINITY;         // NaN
+    }
+    for (int64_t t0 = ((int64_t)blockIdx.x * waves + (threadIdx.x >> 6)) * batch; t0 < a.T;
+         t0 += (int64_t)gridDim.x * waves * batch) {
+        int id = -1;
+        float top = -INFINITY;
+        double sum = 1.0;                                        // of the lane's token (cancels if renormalised)
+        for (int b = 0; b < batch && t0 + b < a.T; ++b) {
+            float l[VPL], z[VPL];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                z[j] = !idle && j * LG + within < gs ? load_logit<DT>(a.logits, (t0 + b) * a.ls + o.first + j * LG) : -INFINITY;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) l[j] = bias[j] > -INFINITY || KIND == kBySoftmax ? z[j] : -INFINITY;
+            if (!choose32<KIND, VPL, KIND == kByLogit && DT != kF32>(a, l, bias, o, b * seg, id))
+                choose64<KIND, VPL>(a, l, bias, o, b * seg, id);
+            if (whole) {
+                float t = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) t = fmaxf(t, z[j]);
+                t = wave_top(t);
+                double y = 0.0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (z[j] > -INFINITY) y += exp((double)z[j] - (double)t);
+                y = wave_total(y);
+                if (own == b) {
+                    top = t;
+                    sum = y;
+                }
+            }
+        }
+        const int64_t token = t0 + own;
+        const float mine = id >= 0 ? load_logit<DT>(a.logits, token * a.ls + id) : -INFINITY;
+        double s = 0.0;
+        if (a.sigmoid) {
+            if (id >= 0) s = sigmoid64(mine);
+        } else {
+            if (a.renormalize) {
+                top = mine;
+                group_steps(seg, [&](auto swap) { top = fmaxf(top, __uint_as_float(swap(__float_as_uint(top)))); });
+            }
+            if (id >= 0) s = exp((double)mine - (double)top) / sum;
+        }
+        if (a.renormalize) {
+            double total = s;
+            group_steps(seg, [&](auto swap) {
+                const uint64_t u = __builtin_bit_cast(uint64_t, total);
+                total += __builtin_bit_cast(double, (uint64_t)swap((uint32_t)(u >> 32)) << 32 | swap((uint32_t)u));
+            });
+            s = total > 0.0 ? s / total : 0.0;
+        }
+        if (q < a.k && own < batch && token < a.T) {
+            a.ids[token * a.k + q] = id;
+            a.w[token * a.k + q] = (float)((double)a.scale * s);
+        }
     }
 }
 
@@ -143,18 +366,26 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int LG, int gs)
 static dim3 token_grid(int T, int waves) { return dim3((unsigned)std::min(((int64_t)T + waves - 1) / waves, (int64_t)1 << 20)); }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-    int LG = 64;
-    while (LG * a.groups > 64) LG >>= 1;
-    const int gs = a.E / a.groups, vpl = (gs + LG - 1) / LG;
-    const int waves = a.T <= 1024 ? 1 : 4;
-    const dim3 grid = token_grid(a.T, waves);
+    const bool grouped = a.top_groups < a.groups;
+    const int kind = !a.bias && !grouped ? kByLogit : (a.sigmoid ? kBySigmoid : kBySoftmax);
+    const int groups = grouped ? a.groups : 1, gs = a.E / groups;
+    int shift = 6;
+    while ((groups << shift) > 64) --shift;
+    const int vpl = (gs + (1 << shift) - 1) >> shift;
+    // few tokens: one a wave, a wave a block; many: as many a wave as their weights have room for
+    const int waves = a.T <= 1024 ? 1 : 4, batch = a.T <= 4096 ? 1 : (a.k <= 16 ? 4 : 2);
     with_dtype(a.dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         auto run = [&](auto v) {
-            hipLaunchKernelGGL((route_kernel<DT, decltype(v)::value>), grid, dim3(64 * waves), 0, s, a, LG, gs);
+            constexpr int VPL = decltype(v)::value;
+            auto go = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, token_grid(a.T, waves * batch), dim3(64 * waves), 0, s, a, shift, gs, batch);
+            };
+            if (kind == kByLogit) go(route_kernel<DT, VPL, kByLogit>);
+            else if (kind == kBySigmoid) go(route_kernel<DT, VPL, kBySigmoid>);
+            else go(route_kernel<DT, VPL, kBySoftmax>);
         };
-        if (vpl <= 1) run(std::integral_constant<int, 1>{});
-        else if (vpl <= 2) run(std::integral_constant<int, 2>{});
+        if (vpl <= 2) run(std::integral_constant<int, 2>{});
         else if (vpl <= 5) run(std::integral_constant<int, 5>{});
         else if (vpl <= 8) run(std::integral_constant<int, 8>{});
         else if (vpl <= 16) run(std::integral_constant<int, 16>{});
@@ -168,74 +399,141 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
 //   renormalised     dl_j = c p_j (dw_j - sum_i p_i dw_i), for sigmoid times 1 - s_j
 //   sigmoid          dl_j = c dw_j s_j (1 - s_j)
 //   softmax          dl_e = s_e (c dw_e - sum_j c s_j dw_j), every expert
-// and 0 elsewhere.  A wave takes a token; it writes the whole row.
+// and 0 elsewhere.  A wave takes a token and writes its whole row, eight experts a lane (one,
+// of fewer than eight); the chosen experts' values reach their lanes through LDS.
 // ---------------------------------------------------------------------------
-template <int DT>
-__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int waves = blockDim.x >> 6;
-    for (int64_t token = (int64_t)blockIdx.x * waves + (threadIdx.x >> 6); token < a.T; token += (int64_t)gridDim.x * waves) {
-    int id = -1;
-    float dw = 0.f, mine = -INFINITY;
-    if (lane < a.k) {
-        id = a.ids[token * a.k + lane];
-        if ((uint32_t)id >= (uint32_t)a.E) id = -1;
-        if (id >= 0) {
-            dw = a.dw[token * a.k + lane];
-            mine = load_logit<DT>(a.logits, token * a.ls + id);
+constexpr int kGradWaves = 4;
+
+// exp(x) to about an ulp: the product's rounding is made good.
+__device__ __forceinline__ float near_exp(float x) {
+    x = fmaxf(x, -200.f);                                         // (0 from there on; no Inf - Inf below)
+    const float t = x * kLog2e, r = fmaf(x, kLog2e, -t), e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, (r + x * 1.92596299e-8f) * 0.693147181f, e);   // (log2 e - kLog2e = 1.926e-8)
+}
+
+// What the wave's lanes have written to LDS is seen by all of them (LDS serves a wave in order).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+template <int DT, int N, int UPL, bool DENSE>
+__global__ __launch_bounds__(64 * kGradWaves) void route_grad_kernel(RouteGradArgs a) {
+    __shared__ __attribute__((aligned(16))) float lds[kGradWaves][UPL * 64 * N];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, units = unit_count<N>(a.E);
+    float* row = lds[wave];
+    for (int64_t token = (int64_t)blockIdx.x * waves + wave; token < a.T; token += (int64_t)gridDim.x * waves) {
+        float l[UPL][N];
+        if (DENSE) {
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+                if (lane + 64 * i < units)
+                    load_unit<DT, N>(a.logits, token * a.ls + unit_begin<N>(lane + 64 * i, a.E), l[i]);
         }
-    }
-    const bool dense = !a.sigmoid && !a.renormalize;
-    float top = -INFINITY, sum = 0.f, g = 0.f, mean = 0.f;        // g: lane q's gradient
-    if (dense) {
-        for (int e = lane; e < a.E; e += 64) top = fmaxf(top, load_logit<DT>(a.logits, token * a.ls + e));
-        top = wave_max_f32(top);
-        for (int e = lane; e < a.E; e += 64) {
-            const float l = load_logit<DT>(a.logits, token * a.ls + e);
-            sum += l > -INFINITY ? expf(l - top) : 0.f;
+        int id = -1;
+        float dw = 0.f, mine = -INFINITY;
+        if (lane < a.k) {
+            id = a.ids[token * a.k + lane];
+            if ((uint32_t)id >= (uint32_t)a.E) id = -1;
+            if (id >= 0) {
+                dw = a.dw[token * a.k + lane];
+                mine = load_logit<DT>(a.logits, token * a.ls + id);
+            }
         }
-        sum = wave_sum_f32(sum);
-        const float s = id >= 0 && mine > -INFINITY ? expf(mine - top) / sum : 0.f;
-        g = a.scale * dw;
-        mean = wave_sum_f32(s * g);
-    } else if (a.renormalize) {
-        float p;
-        if (a.sigmoid) {
-            const double s = id >= 0 ? sigmoid64(mine) : 0.0, total = wave_sum_f64(s);
-            p = total > 0.0 ? (float)(s / total) : 0.f;
+        float mean = 0.f, g = 0.f;                               // g: lane q's gradient
+        if constexpr (DENSE) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+                if (lane + 64 * i < units) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        l[i][e] = sane(l[i][e]);
+                        top = fmaxf(top, l[i][e]);
+                    }
+                }
+            top = wave_top(top);
+#pragma unroll
+            for (int i = 0; i < UPL; ++i) {
+                const int u = lane + 64 * i;
+                if (u >= units) continue;
+                const int old = u * N - unit_begin<N>(u, a.E);    // experts of the unit before
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    l[i][e] = l[i][e] > -INFINITY ? near_exp(l[i][e] - top) : 0.f;
+                    if (e >= old) sum += l[i][e];
+                }
+            }
+            sum = wave_total(sum);
+            const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+#pragma unroll
+                for (int e = 0; e < N; ++e) l[i][e] *= inv;       // scores
+            g = a.scale * dw;
+            mean = wave_total(id >= 0 && mine > -INFINITY ? near_exp(mine - top) * inv * g : 0.f);
+        } else if (a.renormalize) {
+            float p;
+            if (a.sigmoid) {
+                const double s = id >= 0 ? sigmoid64(mine) : 0.0, total = wave_total(s);
+                p = total > 0.0 ? (float)(s / total) : 0.f;
+            } else {
+                const float top = wave_top(mine);
+                p = id >= 0 && mine > -INFINITY ? expf(mine - top) : 0.f;
+                const float total = wave_total(p);
+                p = total > 0.f ? p / total : 0.f;
+            }
+            g = a.scale * p * (dw - wave_total(p * dw));
+            if (a.sigmoid) g *= 1.0f / (1.0f + expf(mine));
         } else {
-            top = wave_max_f32(mine);
-            p = id >= 0 && mine > -INFINITY ? expf(mine - top) : 0.f;
-            const float total = wave_sum_f32(p);
-            p = total > 0.f ? p / total : 0.f;
+            g = id >= 0 ? a.scale * dw / (1.0f + expf(-mine)) / (1.0f + expf(mine)) : 0.f;
         }
-        g = a.scale * p * (dw - wave_sum_f32(p * dw));
-        if (a.sigmoid) g *= 1.0f / (1.0f + expf(mine));
-    } else {
-        g = id >= 0 ? a.scale * dw / (1.0f + expf(-mine)) / (1.0f + expf(mine)) : 0.f;
-    }
-    for (int e = lane; e < ((a.E + 63) & ~63); e += 64) {
-        float v = 0.f;
+        // slots of one expert: the first takes the sum, in slot order
+        bool first = id >= 0;
+        float total = 0.f;
         for (int q = 0; q < a.k; ++q) {
-            const int at = __shfl(id, q, 64);
-            const float add = __shfl(g, q, 64);
-            v += at == e ? add : 0.f;
+            const int other = __builtin_amdgcn_readlane(id, q);
+            const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), q));
+            total += other == id ? v : 0.f;
+            first = first && (other != id || q >= lane);
         }
-        if (e >= a.E) continue;
-        if (dense) {
-            const float l = load_logit<DT>(a.logits, token * a.ls + e);
-            v = l > -INFINITY ? expf(l - top) / sum * (v - mean) : 0.f;
+#pragma unroll
+        for (int i = 0; i < UPL; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) row[(i * 64 + lane) * N + e] = 0.f;
+        wave_sync();
+        if (first) row[id] = total;
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < UPL; ++i) {
+            const int u = lane + 64 * i;
+            if (u >= units) continue;
+            const int c = unit_begin<N>(u, a.E);
+            float v[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = DENSE ? l[i][e] * (row[c + e] - mean) : row[c + e];
+            store_unit<DT, N>(a.dlogits, token * a.ds + c, v);
         }
-        static_cast<typename Elem<DT>::type*>(a.dlogits)[token * a.ds + e] = (typename Elem<DT>::type)from_f32<DT>(v);
-    }
+        wave_sync();
     }
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t s) {
-    const int waves = a.T <= 1024 ? 1 : 4;
-    const dim3 grid = token_grid(a.T, waves);
+    const int waves = a.T <= 1024 ? 1 : kGradWaves;
+    const bool dense = !a.sigmoid && !a.renormalize;
     with_dtype(a.dtype, [&](auto dt) {
-        hipLaunchKernelGGL((route_grad_kernel<decltype(dt)::value>), grid, dim3(64 * waves), 0, s, a);
+        constexpr int DT = decltype(dt)::value;
+        auto run = [&](auto n, auto upl) {
+            constexpr int N = decltype(n)::value, UPL = decltype(upl)::value;
+            if (dense)
+                hipLaunchKernelGGL((route_grad_kernel<DT, N, UPL, true>), token_grid(a.T, waves), dim3(64 * waves), 0, s, a);
+            else
+                hipLaunchKernelGGL((route_grad_kernel<DT, N, UPL, false>), token_grid(a.T, waves), dim3(64 * waves), 0, s, a);
+        };
+        if (a.E < 8) run(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+        else if (a.E <= 512) run(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+        else run(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
     });
     return hipGetLastError();
 }
