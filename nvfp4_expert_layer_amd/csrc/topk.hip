@@ -3,19 +3,23 @@
 //
 // The choice.  A wave takes a token.  With LG = 64 / groups lanes (a power of two) to a group,
 // lane l holds experts gs (l / LG) + LG j + l % LG of groups of gs experts: a group's highest
-// keys meet in LG lanes, and every round of the choice is one maximum over the wave.  Keys are
-// 32-bit integers that order as floats:
-//   without bias and groups, the logits: exact, equal ones go to the lowest id;
+// keys meet in LG lanes.  A lane sorts its keys once; every round of the choice is then one maximum
+// over the wave's first ones (DPP) and a shift in the lane that had it.  Keys are 32-bit integers
+// that order as floats, whose low bits name j:
+//   without bias and groups, the logits (16-bit ones exactly, ties too);
 //   else fp32 scores (hardware exp2 and reciprocal) plus bias.  Each is within
 //     2^-24 (C smax + |key|) of the exact key, with C = 6, smax = 1 for a sigmoid (argument,
 //     exp2, sum, reciprocal; s (1 - s) |l| < 0.23) and C = 40, smax = the highest score for a
-//     softmax of at most 1024 terms.  The choice stands if every two neighbours among the k + 1
-//     highest keys, and the last group in and the first group out, are further apart than their
-//     bounds; else the token is done again in fp64, whose order is the definition's (about one
-//     in a thousand).
-// Weights are fp64 of the chosen logits alone, rounded once.
+//     softmax of at most 1024 terms; and the low bits take up to 2^(BITS - 23) of it.
+// Neighbours among the chosen, and the k-th and the rest, that lie nearer than both bounds are put
+// in order in fp64, whose order is the definition's: of 16384 tokens over 320 experts, 2 have
+// their groups and 21 their experts decided so (a whole choice in fp64 in their place made a call
+// of 1024 tokens take 12 us instead of 6.6).
+// Weights are fp64 of the chosen logits alone, rounded once, for four tokens at a time.
 //
-// Bound by issue: of T=16384 over 320 experts in 8 groups MEASURED
+// Bound by issue: 510 vector instructions a token.  T=16384 over 320 experts in 8 groups: 22 us (51
+// with fp64 keys and a maximum over all of them each round); T=64,
+// no groups: 4.1 us, most of it the chain of one token.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -114,54 +118,68 @@ struct RouteLane {
     int shift, gs, group, first, step;                           // lanes to a group: 1 << shift
 };
 
-// The choice in fp64, by the definition: the q-th expert's id to lane slot + q (-1 stays).
+// ---------------------------------------------------------------------------
+// In fp64, by the definition, where 32 bits leave the order open.
+// ---------------------------------------------------------------------------
+struct Softmax64 {
+    float top;
+    double sum;
+};
 template <int KIND, int VPL>
-__device__ __forceinline__ void choose64(const RouteArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
-                                         const RouteLane& o, int slot, int& id) {
-    const int lane = threadIdx.x & 63, LG = 1 << o.shift;
-    float top = -INFINITY;
-    double sum = 1.0;
+__device__ __forceinline__ Softmax64 softmax64(const float (&l)[VPL]) {
+    Softmax64 z{-INFINITY, 1.0};
     if (KIND == kBySoftmax) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) top = fmaxf(top, l[j]);
-        top = wave_top(top);
-        sum = 0.0;
+        for (int j = 0; j < VPL; ++j) z.top = fmaxf(z.top, l[j]);
+        z.top = wave_top(z.top);
+        double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
-            if (l[j] > -INFINITY) sum += exp((double)l[j] - (double)top);
-        sum = wave_total(sum);
+            if (l[j] > -INFINITY) sum += exp((double)l[j] - (double)z.top);
+        z.sum = wave_total(sum);
     }
-    double key[VPL];
+    return z;
+}
+template <int KIND>
+__device__ __forceinline__ double key64(float l, float bias, const Softmax64& z) {
+    if (KIND == kByLogit || !(l > -INFINITY)) return (double)l;
+    return (KIND == kBySigmoid ? sigmoid64(l) : exp((double)l - (double)z.top) / z.sum) + (double)bias;
+}
+
+// Whether the lane's group is among the best.
+template <int KIND, int VPL>
+__device__ __forceinline__ bool group64(const RouteArgs& a, const double (&key)[VPL], const RouteLane& o) {
+    const int LG = 1 << o.shift;
+    double b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-        key[j] = (double)l[j];
-        if (KIND != kByLogit && l[j] > -INFINITY)
-            key[j] = (KIND == kBySigmoid ? sigmoid64(l[j]) : exp((double)l[j] - (double)top) / sum) + (double)bias[j];
+        b2 = fmax(b2, fmin(b1, key[j]));
+        b1 = fmax(b1, key[j]);
     }
-    if (KIND != kByLogit && a.top_groups < a.groups) {
-        double b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            b2 = fmax(b2, fmin(b1, key[j]));
-            b1 = fmax(b1, key[j]);
-        }
-        for (int i = 1; i < LG; i <<= 1) {
-            const double c1 = __shfl_xor(b1, i, 64), c2 = __shfl_xor(b2, i, 64);
-            b2 = fmax(fmin(b1, c1), fmax(b2, c2));
-            b1 = fmax(b1, c1);
-        }
-        if (a.group_keys == 2 && b2 > -INFINITY) b1 += b2;
-        int ahead = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const double other = __shfl(b1, g * LG, 64);
-            ahead += other > b1 || (other == b1 && g < o.group) ? 1 : 0;
-        }
-        if (ahead >= a.top_groups) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) key[j] = -INFINITY;
-        }
+    for (int i = 1; i < LG; i <<= 1) {
+        const double c1 = __shfl_xor(b1, i, 64), c2 = __shfl_xor(b2, i, 64);
+        b2 = fmax(fmin(b1, c1), fmax(b2, c2));
+        b1 = fmax(b1, c1);
     }
-    if ((uint32_t)(lane - slot) < (uint32_t)a.k) id = -1;
+    if (a.group_keys == 2 && b2 > -INFINITY) b1 += b2;
+    int ahead = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const double other = __shfl(b1, g * LG, 64);
+        ahead += other > b1 || (other == b1 && g < o.group) ? 1 : 0;
+    }
+    return ahead < a.top_groups;
+}
+
+// The choice among the experts of the lanes that are `in`: the q-th expert's id to lane slot + q
+// (-1 stays).
+template <int KIND, int VPL>
+__device__ __forceinline__ void choose64(const RouteArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
+                                         const RouteLane& o, bool in, int slot, int& id) {
+    const int lane = threadIdx.x & 63;
+    const Softmax64 z = softmax64<KIND>(l);
+    double key[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = in ? key64<KIND>(l[j], bias[j], z) : -INFINITY;
     for (int q = 0; q < a.k; ++q) {
         double best = -INFINITY;
         int at = INT_MAX;
@@ -188,16 +206,21 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const float (&l)[VP
     }
 }
 
-// The same from 32-bit keys whose low BITS bits name j, lower ones first; false: not certain.  EXACT
-// (16-bit logits, which leave these bits 0): every key as it is, so nothing is left open; equal
-// ones go by j, then by lane, which is by id where all lanes are one group.
-template <int KIND, int VPL, bool EXACT>
-__device__ __forceinline__ bool choose32(const RouteArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
-                                         const RouteLane& o, int slot, int& id) {
+// The choice: the q-th expert's id to lane slot + q (-1 stays).  32-bit keys, whose low BITS bits
+// name j, lower ones first, give the candidates: the k highest and those that lie too near the
+// k-th to be told from it.  Where two neighbours among them are too near, all candidates are put
+// in order in fp64, a lane each.  EXACT (16-bit logits, which leave the low bits 0): every key as it
+// is, so nothing is left open; equal ones go by j, then by lane, which is by id where all lanes
+// are one group.
+template <int DT, int KIND, int VPL>
+__device__ __forceinline__ void choose(const RouteArgs& a, const typename Elem<DT>::type* row, const float (&l)[VPL],
+                                       const float (&bias)[VPL], const RouteLane& o, int slot, int& id) {
+    constexpr bool EXACT = KIND == kByLogit && DT != kF32;
     constexpr float U = 1.0f / (1 << 24);
     constexpr int BITS = VPL <= 1 ? 0 : (VPL <= 2 ? 1 : (VPL <= 8 ? 3 : 5)), MASK = (1 << BITS) - 1;
     constexpr float R = (2 * (1 << BITS) + 1.02f) * U;           // relative: the low bits, the bias's addition
     const int lane = threadIdx.x & 63, LG = 1 << o.shift;
+    bool in = true;                                              // the lane's group may be chosen from
     float key[VPL], base = 0.f;                                  // base: C smax 2^-24
     if constexpr (KIND == kByLogit) {
 #pragma unroll
@@ -222,72 +245,127 @@ __device__ __forceinline__ bool choose32(const RouteArgs& a, const float (&l)[VP
             key[j] = (KIND == kBySigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[j])) : key[j] * smax) + bias[j];
             if (!(l[j] > -INFINITY)) key[j] = -INFINITY;
         }
-        if (a.top_groups < a.groups) {
-            float b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                b2 = fmaxf(b2, fminf(b1, key[j]));
-                b1 = fmaxf(b1, key[j]);
-            }
-            group_steps(LG, [&](auto swap) {
-                const float c1 = __uint_as_float(swap(__float_as_uint(b1))), c2 = __uint_as_float(swap(__float_as_uint(b2)));
-                b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
-                b1 = fmaxf(b1, c1);
-            });
-            const bool two = a.group_keys == 2 && b2 > -INFINITY, any = b1 > -INFINITY;
-            const float own = two ? b1 + b2 : b1;
-            // what the sum may be off by
-            const float off = !any ? 0.f : (two ? 2.f * base + (fabsf(b1) + fabsf(b2) + fabsf(own)) * U * 1.01f
-                                                : base + fabsf(b1) * U * 1.01f);
-            int ahead = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const float other =
-                    __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(own), g << o.shift));
-                ahead += other > own ? 1 : 0;                    // (equal ones in and out are not certain)
-            }
-            const bool live = o.group < a.groups, in = live && ahead < a.top_groups;
-            const float last_in = -wave_top(in ? -(own - off) : -INFINITY);
-            const float first_out = wave_top(live && !in ? own + off : -INFINITY);
-            if (!(last_in > first_out)) return false;
-            if (!in) {
-#pragma unroll
-                for (int j = 0; j < VPL; ++j) key[j] = -INFINITY;
-            }
-        }
     }
     uint32_t u[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) u[j] = (order_bits(key[j]) & ~(uint32_t)MASK) | (uint32_t)(VPL - 1 - j);
-    uint32_t got = 0, from = 0, after = 0;                       // lane slot + q: the q-th key and its lane
-    for (int q = 0; q <= a.k; ++q) {
-        uint32_t m = 0;
+    // a lane's keys, highest first: a group's two highest and every round's candidate are then at hand
+    // (many keys a lane: the maximum of all each time)
+    constexpr bool SORTED = VPL <= 8;
+    if constexpr (SORTED) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) m = m > u[j] ? m : u[j];
-        after = wave_max_u32(m);
-        if (after < kKeys || q == a.k) break;
-        const uint64_t who = __ballot(m == after);
-        if (!EXACT && (who & (who - 1))) return false;
-        const int w = __ffsll((unsigned long long)who) - 1;
-        if (lane == slot + q) {
-            got = after;
+        for (int pass = 0; pass < VPL; ++pass)
+#pragma unroll
+            for (int j = pass & 1; j + 1 < VPL; j += 2) {
+                const uint32_t x = u[j], y = u[j + 1];
+                u[j] = x > y ? x : y;
+                u[j + 1] = x > y ? y : x;
+            }
+    }
+    if (KIND != kByLogit && a.top_groups < a.groups) {
+        uint32_t u1 = u[0], u2 = SORTED ? u[1] : 0u;
+        if (!SORTED) {
+#pragma unroll
+            for (int j = 1; j < VPL; ++j) {
+                const uint32_t low = u1 < u[j] ? u1 : u[j];
+                u2 = u2 > low ? u2 : low;
+                u1 = u1 > u[j] ? u1 : u[j];
+            }
+        }
+        group_steps(LG, [&](auto swap) {
+            const uint32_t c1 = swap(u1), c2 = swap(u2), low = u1 < c1 ? u1 : c1, high = u2 > c2 ? u2 : c2;
+            u2 = low > high ? low : high;
+            u1 = u1 > c1 ? u1 : c1;
+        });
+        const bool any = u1 >= kKeys, two = a.group_keys == 2 && u2 >= kKeys;
+        const float b1 = order_value(u1), b2 = two ? order_value(u2) : 0.f, own = b1 + b2;
+        // what the sum may be off by; groups without keys come last
+        const float off = (two ? 2.f : 1.f) * base + (fabsf(b1) + fabsf(b2)) * (R + 1.01f * U) + 1e-36f;
+        const uint32_t sum = any ? order_bits(own) : 0u;
+        int ahead = 0;
+        for (int g = 0; g < a.groups; ++g)
+            ahead += (uint32_t)__builtin_amdgcn_readlane((int)sum, g << o.shift) > sum ? 1 : 0;
+        const bool live = o.group < a.groups;
+        in = ahead < a.top_groups;
+        const uint32_t last_in = ~wave_max_u32(in && live ? ~(any ? order_bits(own - off) : 0u) : 0u);
+        const uint32_t first_out = wave_max_u32(in || !live ? 0u : (any ? order_bits(own + off) : 1u));
+        // (equal sums may let too many in)
+        if (!(last_in > first_out) || __popcll(__ballot(in && live)) != a.top_groups << o.shift) {
+            const Softmax64 z = softmax64<KIND>(l);
+            double key[VPL];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) key[j] = key64<KIND>(l[j], bias[j], z);
+            in = group64<KIND>(a, key, o);
+        }
+        if (!in) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) u[j] = 0;
+        }
+    }
+    uint32_t got = 0, from = 0;                                  // lane q: the q-th key and its lane
+    float last = 0.f;                                            // the k-th key
+    int n = 0;
+    for (;; ++n) {
+        uint32_t m = u[0];
+        if (!SORTED) {
+#pragma unroll
+            for (int j = 1; j < VPL; ++j) m = m > u[j] ? m : u[j];
+        }
+        const uint32_t best = wave_max_u32(m);
+        if (best < kKeys) break;
+        if (n >= a.k) {
+            if (EXACT) break;
+            const float now = order_value(best);
+            if (last - now > 2.f * base + (fabsf(last) + fabsf(now)) * R + 1e-36f) break;
+            if (n == 64) break;                                  // too many that are too near
+        }
+        if (!EXACT && n == a.k - 1) last = order_value(best);
+        const int w = __ffsll((unsigned long long)__ballot(m == best)) - 1;
+        if (lane == n) {
+            got = best;
             from = (uint32_t)w;
         }
-        const bool mine = lane == w;
+        const uint32_t mine = lane == w ? ~0u : 0u;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) u[j] = mine && u[j] == after ? 0u : u[j];
+        for (int j = 0; j < VPL; ++j) {
+            // (as bits: the compiler would turn a choice of neighbours into a search for one)
+            if (SORTED) u[j] = (u[j] & ~mine) | ((j + 1 < VPL ? u[j + 1] : 0u) & mine);
+            else u[j] = u[j] == best ? u[j] & ~mine : u[j];
+        }
     }
-    const int q = lane - slot;
-    const bool ours = (uint32_t)q < (uint32_t)a.k && got >= kKeys;
-    if (!EXACT) {
-        // every key further from the next than both may be off by
-        uint32_t next = (uint32_t)__shfl_down((int)got, 1, 64);
-        if (q == a.k - 1) next = after;
+    if (n == 64) {
+        choose64<KIND>(a, l, bias, o, in, slot, id);
+        return;
+    }
+    const int at = lane < n ? (int)(from >> o.shift) * o.gs + (VPL - 1 - (int)(got & MASK)) * LG + (int)(from & (LG - 1)) : -1;
+    if constexpr (!EXACT) {
+        // every key further from the next than both may be off by?
+        const uint32_t next = (uint32_t)__shfl_down((int)got, 1, 64);
         const float x = order_value(got), y = order_value(next);
-        const bool open = ours && next >= kKeys && !(x - y > 2.f * base + (fabsf(x) + fabsf(y)) * R + 1e-36f);
-        if (__ballot(open)) return false;
+        const bool open = lane + 1 < n && !(x - y > 2.f * base + (fabsf(x) + fabsf(y)) * R + 1e-36f);
+        if (__ballot(open)) {
+            const Softmax64 z = softmax64<KIND>(l);
+            const double key = lane < n ? key64<KIND>(load_logit<DT>(row, at),
+                                                      KIND != kByLogit && a.bias ? a.bias[at] : 0.f, z) : 0.0;
+            const uint64_t bits = __builtin_bit_cast(uint64_t, key);
+            int rank = 0;
+            for (int c = 0; c < n; ++c) {
+                const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), c);
+                const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)bits, c);
+                const double other = __builtin_bit_cast(double, hi << 32 | lo);
+                rank += other > key || (other == key && __builtin_amdgcn_readlane(at, c) < at) ? 1 : 0;
+            }
+            for (int q = 0; q < a.k; ++q) {
+                const uint64_t who = __ballot(lane < n && rank == q);
+                if (!who) break;
+                const int e = __builtin_amdgcn_readlane(at, __ffsll((unsigned long long)who) - 1);
+                if (lane == slot + q) id = e;
+            }
+            return;
+        }
     }
-    if (ours) id = (int)(from >> o.shift) * o.gs + (VPL - 1 - (int)(got & MASK)) * LG + (int)(from & (LG - 1));
-    return true;
+    const int moved = __shfl(at, lane - slot, 64);
+    if ((uint32_t)(lane - slot) < (uint32_t)a.k) id = moved;
 }
 
 // A wave takes `batch` tokens one after another; their weights, a token's in a segment of 16 (k up
@@ -295,30 +373,35 @@ __device__ __forceinline__ bool choose32(const RouteArgs& a, const float (&l)[VP
 template <int DT, int VPL, int KIND>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int shift, int gs, int batch) {
     const int lane = threadIdx.x & 63, LG = 1 << shift, group = lane >> shift, within = lane & (LG - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);       // (scalar row addresses)
     const int waves = blockDim.x >> 6, seg = a.k <= 16 ? 16 : 32, q = lane & (seg - 1), own = lane >> (a.k <= 16 ? 4 : 5);
     const RouteLane o{shift, gs, group, group * gs + within, LG};
     const bool whole = !a.sigmoid && !a.renormalize;             // weights need every expert's score
     const bool idle = group * gs >= a.E;
     float bias[VPL];
+    int at[VPL];                                                 // the lane's experts; idle places read the token's first
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
+        at[j] = idle || j * LG + within >= gs ? 0 : o.first + j * LG;
         bias[j] = idle || j * LG + within >= gs ? -INFINITY : (KIND != kByLogit && a.bias ? a.bias[o.first + j * LG] : 0.f);
         if (!(bias[j] > -INFINITY)) bias[j] = -INFINITY;         // NaN
     }
-    for (int64_t t0 = ((int64_t)blockIdx.x * waves + (threadIdx.x >> 6)) * batch; t0 < a.T;
+    for (int64_t t0 = ((int64_t)blockIdx.x * waves + wave) * batch; t0 < a.T;
          t0 += (int64_t)gridDim.x * waves * batch) {
         int id = -1;
         float top = -INFINITY;
         double sum = 1.0;                                        // of the lane's token (cancels if renormalised)
         for (int b = 0; b < batch && t0 + b < a.T; ++b) {
+            const typename Elem<DT>::type* row = static_cast<const typename Elem<DT>::type*>(a.logits) + (t0 + b) * a.ls;
             float l[VPL], z[VPL];
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                z[j] = !idle && j * LG + within < gs ? load_logit<DT>(a.logits, (t0 + b) * a.ls + o.first + j * LG) : -INFINITY;
+            for (int j = 0; j < VPL; ++j) z[j] = load_logit<DT>(row, at[j]);
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) l[j] = bias[j] > -INFINITY || KIND == kBySoftmax ? z[j] : -INFINITY;
-            if (!choose32<KIND, VPL, KIND == kByLogit && DT != kF32>(a, l, bias, o, b * seg, id))
-                choose64<KIND, VPL>(a, l, bias, o, b * seg, id);
+            for (int j = 0; j < VPL; ++j) {
+                if (o.first + j * LG != at[j]) z[j] = -INFINITY;
+                l[j] = bias[j] > -INFINITY || KIND == kBySoftmax ? z[j] : -INFINITY;
+            }
+            choose<DT, KIND, VPL>(a, row, l, bias, o, b * seg, id);
             if (whole) {
                 float t = -INFINITY;
 #pragma unroll
@@ -373,7 +456,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
     while ((groups << shift) > 64) --shift;
     const int vpl = (gs + (1 << shift) - 1) >> shift;
     // few tokens: one a wave, a wave a block; many: as many a wave as their weights have room for
-    const int waves = a.T <= 1024 ? 1 : 4, batch = a.T <= 4096 ? 1 : (a.k <= 16 ? 4 : 2);
+    // (groups, us with 1, 2, 4 a wave: T=4096 9.2 / 9.8 / 9.8, T=8192 14.6 / 13.1 / 15.6, T=16384 24.5 / 22.0
+    // / 20.9, T=65536 88 / 75 / 70)
+    const int waves = a.T <= 1024 ? 1 : 4, batch = a.T <= 4096 ? 1 : (a.k <= 16 && a.T >= 16384 ? 4 : 2);
     with_dtype(a.dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         auto run = [&](auto v) {
