@@ -1,7 +1,7 @@
 // MXFP8 quantizer and dequantizer (gfx950): E4M3 codes, one E8M0 scale per 32 elements.
 //
 // Both are bound by memory and laid out as MXFP4's: eight elements a thread, four
-// neighbouring threads a block.
+// neighbouring threads a block.  65536 x 4096 from bf16 135 us (6.0 TB/s), back 124 us (6.5).
 #include "block.h"
 #include "eights.h"
 #include "mx_common.h"
