@@ -37,7 +37,8 @@ extern "C" {
  * An expert whose logit or bias is NaN or -Inf has no key and is never chosen (a logit of
  * NaN or -Inf has score 0).  A logit of +Inf counts as the largest finite fp32.  Where
  * fewer than top_k experts have keys the last ids are -1, their weights 0 (a group
- * without keys comes last); chosen scores that sum to 0 give weights of 0.
+ * without keys comes last; of groups with equal sums the lower one is first); chosen scores
+ * that sum to 0 give weights of 0.
  *
  * The order is that of the exact keys: keys are compared in fp64, or by their logits
  * where no bias and no groups are given.  (moe_dispatch drops ids of -1, moe_combine does
@@ -72,7 +73,9 @@ int moe_route_backward(const moe_route_problem *p, const void *logits, int64_t l
 
 /* ------------------------------------------------------------------------- *
  * Norm.  h = x + residual (rounded to the rows' type; h = x without a residual),
- *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight.
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight,
+ * in fp32: from magnitudes of about 2^63 on the squares' sum passes its range (rstd 0), below
+ * 2^-63 they leave no trace beside eps, and with eps 0 a row of zeros has y NaN.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t rows;           /* T: 0..2^27                                             */

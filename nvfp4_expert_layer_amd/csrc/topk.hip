@@ -289,8 +289,9 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const typename Elem<D
         in = ahead < a.top_groups;
         const uint32_t last_in = ~wave_max_u32(in && live ? ~(any ? order_bits(own - off) : 0u) : 0u);
         const uint32_t first_out = wave_max_u32(in || !live ? 0u : (any ? order_bits(own + off) : 1u));
-        // (equal sums may let too many in)
-        if (!(last_in > first_out) || __popcll(__ballot(in && live)) != a.top_groups << o.shift) {
+        // (equal sums may let too many in; a key of +Inf or a sum past fp32 has no bound)
+        if (!(last_in > first_out) || __popcll(__ballot(in && live)) != a.top_groups << o.shift ||
+            __ballot(any && !(fabsf(own) + off <= FLT_MAX))) {
             const Softmax64 z = softmax64<KIND>(l);
             double key[VPL];
 #pragma unroll

@@ -259,3 +259,36 @@ def test_gradient_against_differences():
                 # the third derivative is at most 2 sum |dw|, a weight rounds by 2^-24
                 lim = (2 * h * h / 6 + 2 ** -24 / h) * float(dw[t].abs().sum())
                 assert abs((val[0] - val[1]) / (2 * h) - got[t, e]) <= lim
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_keys", [1, 2])
+@pytest.mark.parametrize("groups,E,top", [(8, 320, 4), (8, 320, 1), (4, 64, 1), (2, 10, 1), (64, 128, 9), (2, 1024, 1)])
+def test_biases_beyond_a_sum(kind, group_keys, groups, E, top):
+    """Biases of +Inf, and of magnitudes whose sums pass fp32: a group's sum is that of the keys in fp64, equal
+    sums (two of +Inf) go to the lower group."""
+    require_gpu()
+    log(f"route biases {kind} groups={groups} E={E} top={top} keys={group_keys}")
+    n = E // groups
+    for case in range(8):
+        logits, bias = draw(5, E, torch.float32, 50 + case)
+        if case == 0:                                            # more groups with +Inf than may serve
+            bias[n - 1::n] = float("inf")
+        elif case == 1:                                          # two in the last group: no more than one
+            bias[0], bias[-1], bias[-2] = float("inf"), float("inf"), float("inf")
+        elif case == 2:
+            bias = torch.full_like(bias, 3e38)
+        elif case == 3:                                          # sums of 4e38 to 6.8e38 and of the same below 0
+            bias = torch.linspace(2.0e38, 3.4e38, E) * torch.where(torch.arange(E) % 3 == 0, -1.0, 1.0)
+        elif case == 4:
+            bias = torch.linspace(-3.4e38, -2.0e38, E)
+        elif case == 5:                                          # +Inf once a group, at other places of each
+            bias[torch.arange(groups) * n + torch.arange(groups - 1, -1, -1) * (n - 1) // (groups - 1)] = float("inf")
+        elif case == 6:                                          # sums past fp32, equal, at other places of each
+            bias[torch.arange(groups) * n + torch.arange(groups - 1, -1, -1) * (n - 1) // (groups - 1)] = 3.4e38
+            bias[torch.arange(groups) * n + torch.arange(groups) * (n - 1) // (groups - 1)] = 3.4e38
+        else:                                                    # the highest keys in the last groups, by little
+            bias = 3.4e38 - torch.arange(E).flip(0) * 1e35
+            bias[::n] = float("inf")
+        check(logits, bias, min(top * n, 5), kind, groups=groups, top_groups=top, group_keys=group_keys)
+        check(logits, bias, min(E, 5), kind)
