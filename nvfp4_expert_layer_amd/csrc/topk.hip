@@ -17,9 +17,10 @@
 // of 1024 tokens take 12 us instead of 6.6).
 // Weights are fp64 of the chosen logits alone, rounded once, for four tokens at a time.
 //
-// Bound by issue: 510 vector instructions a token.  T=16384 over 320 experts in 8 groups: 22 us (51
-// with fp64 keys and a maximum over all of them each round); T=64,
-// no groups: 4.1 us, most of it the chain of one token.
+// Bound by issue: 445 vector instructions a token.  T=16384 over 320 experts in 8 groups: 18.4 us (51
+// with fp64 keys and a maximum over all of them each round; 21.1 with every logit made sane and the
+// search for near ones in the rounds up to k); T=64, no groups: 4.1 us, most of it the chain of one
+// token.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -142,7 +143,8 @@ __device__ __forceinline__ Softmax64 softmax64(const float (&l)[VPL]) {
 }
 template <int KIND>
 __device__ __forceinline__ double key64(float l, float bias, const Softmax64& z) {
-    if (KIND == kByLogit || !(l > -INFINITY)) return (double)l;
+    if (!(l > -INFINITY)) return -INFINITY;
+    if (KIND == kByLogit) return (double)l;
     return (KIND == kBySigmoid ? sigmoid64(l) : exp((double)l - (double)z.top) / z.sum) + (double)bias;
 }
 
@@ -206,7 +208,8 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const float (&l)[VP
     }
 }
 
-// The choice: the q-th expert's id to lane slot + q (-1 stays).  32-bit keys, whose low BITS bits
+// The choice from the lane's logits l (by a sigmoid: as they lie in memory; else sane ones, -Inf in
+// idle places): the q-th expert's id to lane slot + q (-1 stays).  32-bit keys, whose low BITS bits
 // name j, lower ones first, give the candidates: the k highest and those that lie too near the
 // k-th to be told from it.  Where two neighbours among them are too near, all candidates are put
 // in order in fp64, a lane each.  EXACT (16-bit logits, which leave the low bits 0): every key as it
@@ -290,8 +293,9 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const typename Elem<D
         const uint32_t last_in = ~wave_max_u32(in && live ? ~(any ? order_bits(own - off) : 0u) : 0u);
         const uint32_t first_out = wave_max_u32(in || !live ? 0u : (any ? order_bits(own + off) : 1u));
         // (equal sums may let too many in; a key of +Inf or a sum past fp32 has no bound)
-        if (!(last_in > first_out) || __popcll(__ballot(in && live)) != a.top_groups << o.shift ||
-            __ballot(any && !(fabsf(own) + off <= FLT_MAX))) {
+        if (!(last_in > first_out) ||
+            __popcll(__builtin_amdgcn_ballot_w64(in && live)) != a.top_groups << o.shift ||
+            __builtin_amdgcn_ballot_w64(any && !(fabsf(own) + off <= FLT_MAX))) {
             const Softmax64 z = softmax64<KIND>(l);
             double key[VPL];
 #pragma unroll
@@ -304,24 +308,19 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const typename Elem<D
         }
     }
     uint32_t got = 0, from = 0;                                  // lane q: the q-th key and its lane
-    float last = 0.f;                                            // the k-th key
     int n = 0;
-    for (;; ++n) {
-        uint32_t m = u[0];
+    uint32_t m, best;                                            // the lane's and the wave's highest key
+    auto highest = [&]() {
+        m = u[0];
         if (!SORTED) {
 #pragma unroll
             for (int j = 1; j < VPL; ++j) m = m > u[j] ? m : u[j];
         }
-        const uint32_t best = wave_max_u32(m);
-        if (best < kKeys) break;
-        if (n >= a.k) {
-            if (EXACT) break;
-            const float now = order_value(best);
-            if (last - now > 2.f * base + (fabsf(last) + fabsf(now)) * R + 1e-36f) break;
-            if (n == 64) break;                                  // too many that are too near
-        }
-        if (!EXACT && n == a.k - 1) last = order_value(best);
-        const int w = __ffsll((unsigned long long)__ballot(m == best)) - 1;
+        best = wave_max_u32(m);
+        return best >= kKeys;
+    };
+    auto take = [&]() {                                          // it becomes the n-th
+        const int w = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m == best));
         if (lane == n) {
             got = best;
             from = (uint32_t)w;
@@ -332,6 +331,16 @@ __device__ __forceinline__ void choose(const RouteArgs& a, const typename Elem<D
             // (as bits: the compiler would turn a choice of neighbours into a search for one)
             if (SORTED) u[j] = (u[j] & ~mine) | ((j + 1 < VPL ? u[j + 1] : 0u) & mine);
             else u[j] = u[j] == best ? u[j] & ~mine : u[j];
+        }
+    };
+    for (; n < a.k && highest(); ++n) take();
+    if (!EXACT && n == a.k) {                                    // and those too near to the k-th
+        const float last = order_value((uint32_t)__builtin_amdgcn_readlane((int)got, n - 1));
+        for (; highest(); ++n) {
+            const float now = order_value(best);
+            if (last - now > 2.f * base + (fabsf(last) + fabsf(now)) * R + 1e-36f) break;
+            if (n == 64) break;                                  // too many
+            take();
         }
     }
     if (n == 64) {
@@ -379,12 +388,15 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int shift, int 
     const RouteLane o{shift, gs, group, group * gs + within, LG};
     const bool whole = !a.sigmoid && !a.renormalize;             // weights need every expert's score
     const bool idle = group * gs >= a.E;
+    typedef typename Elem<DT>::type L;
     float bias[VPL];
-    int at[VPL];                                                 // the lane's experts; idle places read the token's first
+    uint32_t at[VPL];                                            // bytes to the lane's logits; idle places read the token's first
+    bool here[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-        at[j] = idle || j * LG + within >= gs ? 0 : o.first + j * LG;
-        bias[j] = idle || j * LG + within >= gs ? -INFINITY : (KIND != kByLogit && a.bias ? a.bias[o.first + j * LG] : 0.f);
+        here[j] = !idle && j * LG + within < gs;
+        at[j] = here[j] ? (o.first + j * LG) * (uint32_t)sizeof(L) : 0u;
+        bias[j] = !here[j] ? -INFINITY : (KIND != kByLogit && a.bias ? a.bias[o.first + j * LG] : 0.f);
         if (!(bias[j] > -INFINITY)) bias[j] = -INFINITY;         // NaN
     }
     for (int64_t t0 = ((int64_t)blockIdx.x * waves + wave) * batch; t0 < a.T;
@@ -393,25 +405,25 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int shift, int 
         float top = -INFINITY;
         double sum = 1.0;                                        // of the lane's token (cancels if renormalised)
         for (int b = 0; b < batch && t0 + b < a.T; ++b) {
-            const typename Elem<DT>::type* row = static_cast<const typename Elem<DT>::type*>(a.logits) + (t0 + b) * a.ls;
-            float l[VPL], z[VPL];
+            const L* row = static_cast<const L*>(a.logits) + (t0 + b) * a.ls;
+            float l[VPL];
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) z[j] = load_logit<DT>(row, at[j]);
+            for (int j = 0; j < VPL; ++j)
+                l[j] = to_f32<DT>(*reinterpret_cast<const L*>(reinterpret_cast<const char*>(row) + at[j]));
+            if (KIND != kBySigmoid) {                            // (there a bias or logit of NaN or -Inf shows in the key)
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                if (o.first + j * LG != at[j]) z[j] = -INFINITY;
-                l[j] = bias[j] > -INFINITY || KIND == kBySoftmax ? z[j] : -INFINITY;
+                for (int j = 0; j < VPL; ++j) l[j] = here[j] ? sane(l[j]) : -INFINITY;
             }
             choose<DT, KIND, VPL>(a, row, l, bias, o, b * seg, id);
             if (whole) {
                 float t = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) t = fmaxf(t, z[j]);
+                for (int j = 0; j < VPL; ++j) t = fmaxf(t, l[j]);
                 t = wave_top(t);
                 double y = 0.0;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)
-                    if (z[j] > -INFINITY) y += exp((double)z[j] - (double)t);
+                    if (l[j] > -INFINITY) y += exp((double)l[j] - (double)t);
                 y = wave_total(y);
                 if (own == b) {
                     top = t;
@@ -457,8 +469,8 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
     while ((groups << shift) > 64) --shift;
     const int vpl = (gs + (1 << shift) - 1) >> shift;
     // few tokens: one a wave, a wave a block; many: as many a wave as their weights have room for
-    // (groups, us with 1, 2, 4 a wave: T=4096 9.2 / 9.8 / 9.8, T=8192 14.6 / 13.1 / 15.6, T=16384 24.5 / 22.0
-    // / 20.9, T=65536 88 / 75 / 70)
+    // (groups, us with 1, 2, 4 a wave: T=4096 8.3 / 9.2 / 12.8, T=8192 12.8 / 11.8 / 14.4, T=16384 22.3 / 19.4
+    // / 18.5, T=65536 76 / 65 / 61)
     const int waves = a.T <= 1024 ? 1 : 4, batch = a.T <= 4096 ? 1 : (a.k <= 16 && a.T >= 16384 ? 4 : 2);
     with_dtype(a.dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
