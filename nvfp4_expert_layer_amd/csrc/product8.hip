@@ -82,15 +82,17 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
     const int sdst = k8OffS + (wave < 4 ? 0 : k8Scales);
     Tile wt;                                             // the tile of the next weight loads
     uint32_t wshift = 0, ashift = 0;                     // !ALIGNED: the lane's scale rows' first byte in a dword
+    auto scales_from = [&](const Tile& n) {
+        if (ALIGNED) return;
+        const uintptr_t w = reinterpret_cast<uintptr_t>(p.w_s) + ((int64_t)n.g * p.N + n.nt * kTN) * KB;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p.a_s) + (int64_t)n.rb * KB;
+        wshift = ((uint32_t)w + r32 * KB) & 3;
+        ashift = ((uint32_t)a + r32 * KB) & 3;
+    };
     auto rows_from = [&](const Tile& n) {
         abase = static_cast<const uint8_t*>(p.a) + (int64_t)n.rb * p.K;
         amax = n.re - 1 - n.rb;
-        if (!ALIGNED) {                                  // (the rows' loads are one chunk ahead, as are the scales read)
-            const uintptr_t w = reinterpret_cast<uintptr_t>(p.w_s) + ((int64_t)n.g * p.N + n.nt * kTN) * KB;
-            const uintptr_t a = reinterpret_cast<uintptr_t>(p.a_s) + (int64_t)n.rb * KB;
-            wshift = ((uint32_t)w + r32 * KB) & 3;
-            ashift = ((uint32_t)a + r32 * KB) & 3;
-        }
+        scales_from(n);                                  // (the rows' loads are one chunk ahead, as are the scales read)
     };
     auto weight_from = [&](const Tile& n) {
         wt = n;
@@ -291,12 +293,16 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     tokens(0, c0);
+    const uint32_t wlater = wshift, alater = ashift;     // (a tile of one chunk: the rows' loads have come to the next)
+    scales_from(t);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         weights(0, 0, 0, j);
         scales(0, j);
     }
     take_scales();
+    wshift = wlater;
+    ashift = alater;
     for (;;) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)

@@ -171,3 +171,14 @@ def test_no_rows():
     q = nv.MXFP8Rows.empty(0, 64)
     nv.moe_mxfp8_product(nv.make_product_problem(0, 16, 64, 2), q, w, torch.zeros(3, dtype=torch.int32, device="cuda"),
                          torch.empty(0, 16, device="cuda"))
+
+
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 192, 224, 256, 288, 480, 544, 800])
+@pytest.mark.parametrize("M,N,G", [(3026, 841, 66), (4100, 515, 100), (1200, 4099, 20), (90000, 257, 3)])
+def test_workgroups_of_several_tiles(M, N, G, K):
+    """More tiles than compute units: scale rows that lie differently to dwords in a workgroup's tiles, of one
+    chunk of K and more."""
+    require_gpu()
+    log(f"product8 several tiles M={M} N={N} G={G} K={K}")
+    assert not nv.lib().moe_internal_product_streams(M, N, K, G, K, 2, 0, 256)
+    check(M, N, K, spread(M, G, K, M - 5))
