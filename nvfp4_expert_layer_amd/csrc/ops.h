@@ -79,6 +79,7 @@ struct ProductArgs {
 hipError_t launch_product(const ProductArgs& p, int cus, hipStream_t s);
 hipError_t launch_product_tiles(const ProductArgs& p, int cus, hipStream_t s);  // many rows a group
 hipError_t launch_product8_tiles(const ProductArgs& p, int cus, hipStream_t s);
+bool product8_dwords(const ProductArgs& p);      // whether MXFP8 rows' and the weight's scales can be read in dwords
 hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s);
 hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t s);
 
@@ -89,3 +90,5 @@ hipError_t launch_product_grad_tiles(const ProductArgs& p, int cus, hipStream_t 
 // tests can say which kernel their shapes reach.  mx: 0 bf16 rows, 1 MXFP4, 2 MXFP8.
 extern "C" int moe_internal_product_streams(int M, int N, int K, int G, int64_t stride, int mx, int backward,
                                             int cus);
+// Of a product of MXFP8 rows in tiles: whether they are the short ones.
+extern "C" int moe_internal_product8_short(int M, int N, int K, int G, int cus);

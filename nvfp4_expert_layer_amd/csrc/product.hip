@@ -461,14 +461,20 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // can pick the slower kernel (W4A16, 160 experts of 2048 x 4096: 3500 rows 198 / 236 spread
 // evenly, 572 / 324 after a Zipf law; 40 of 320 experts, an eighth of 2048 rows kept, 47 / 71).
 //
-// MXFP8 rows: the tile kernel's stages are half as deep, so one tile alone takes longer (one
-// of K = 4096: 40 us) and streaming wins for more rows.  Streamed / tiled: 160 groups of 2048 x
-// 4096 160 / 222 at 32 rows a group, 275 / 236 at 48; 64 groups 60 / 90 and 102 / 97; with the
-// tiles of one row block on a quarter of the card (8 groups) 37 / 43 at 96, 48 / 43 at 128; on a
-// twelfth or less (one group of 4096 x 4096) 45 / 48 at 192, 59 / 49 at 256.
+// MXFP8 rows in short tiles (scales in dwords), streamed / tiled us: where one row block of every
+// group fills the card twice, 173 / 154 at 8 rows a group (320 of 4096 x 1024), 277 / 269 (320 of 2048
+// x 4096), 51 / 51 at 12 (64 of 2048 x 4096), 322 / 282 at 24; at half a card (16 groups) 18 / 20 at
+// 20, 29 / 21 at 24; at a quarter (8 groups) 24 / 25 at 48, 31 / 25 at 56; at a sixteenth (one group
+// of 4096 x 4096) 24 / 24 at 96, 30 / 24 at 128.
+// In the tall ones one tile alone takes longer (one of K = 4096: 40 us) and streaming wins for more
+// rows: 160 groups of 2048 x 4096 160 / 222 at 32 rows a group, 275 / 236 at 48; 64 groups 60 / 90
+// and 102 / 97; a quarter of the card (8 groups) 37 / 43 at 96, 48 / 43 at 128; a twelfth or less
+// (one group of 4096 x 4096) 45 / 48 at 192, 59 / 49 at 256.
 static bool streamed(const ProductArgs& p, int cus) {
     if (p.a8) {
         const int64_t one = (int64_t)p.G * ((p.N + 255) / 256);
+        if (product8_dwords(p))
+            return p.M <= (int64_t)p.G * (one >= 2 * cus ? 8 : (one * 3 >= cus ? 20 : (one * 8 >= cus ? 48 : 96)));
         return p.M <= (int64_t)p.G * (one * 12 <= cus ? 200 : (one * 4 <= cus ? 110 : 40));
     }
     const int rows = p.a_s ? 20 : 24;
@@ -498,7 +504,7 @@ hipError_t launch_product_grad(const ProductArgs& p, int cus, hipStream_t s) {
 
 int moe_internal_product_streams(int M, int N, int K, int G, int64_t stride, int mx, int backward, int cus) {
     moe::ProductArgs p{};
-    const uint8_t scales = 0;
+    alignas(16) const uint8_t scales = 0;
     p.M = M; p.N = N; p.K = K; p.G = G; p.as = stride;
     p.a_s = mx ? &scales : nullptr;
     p.a8 = mx == 2;

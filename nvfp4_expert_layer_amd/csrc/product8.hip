@@ -1,5 +1,5 @@
-// Products of MXFP8 rows with MXFP4 weights (W4A8) in tiles, for many rows a group (gfx950).
-// A tile is 256 rows of one group x 256 outputs; eight waves of 64 rows x 128 outputs, one
+// Products of MXFP8 rows with MXFP4 weights (W4A8) in tiles, for more rows a group than are worth
+// streaming for (gfx950).  A tile is 256 rows of one group x 256 outputs; eight waves of 64 rows x 128 outputs, one
 // workgroup a CU; the operands come straight from global memory to LDS.
 //
 //   32x32x64 scaled MFMAs take both formats as they lie in memory (half the rate of FP4 x FP4,
@@ -330,12 +330,201 @@ __global__ __launch_bounds__(kTThreads) void w4a8_tile_kernel(ProductArgs p) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Short tiles: 64 rows x 256 outputs, for groups of some dozens of rows, where the weight's bytes
+// are the cost and what counts is how many of them are under way: three stages of 256 k, of which
+// two load while one is multiplied (the tiles above have one under way on average).  A wave takes
+// 32 outputs and all rows.  Scale rows that can be read in dwords only (as ALIGNED above).  24 / 48
+// rows a group over 320 experts of 2048 x 4096: 282 / 345 us, 5.3 / 4.6 TB/s (a large copy: 4.95).
+// ---------------------------------------------------------------------------
+constexpr int kSM = 64;
+// a stage: weight [256][128 bytes] | rows [2 halves][64][128 bytes] | weight scales [256][8] | rows' [64][8]
+constexpr int kSRows = 256 * 128, kSWs = kSRows + 2 * kSM * 128, kSAs = kSWs + 256 * 8, kSStage = kSAs + kSM * 8;
+constexpr int kSTable = 3 * kSStage, kSLds = kSTable + kTable;
+constexpr int kSLoads = 8;                               // a wave's of a stage
+
+__global__ __launch_bounds__(kTThreads) void w4a8_short_kernel(ProductArgs p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, r32 = lane & 31, NT = (p.N + kTN - 1) / kTN, KB = p.K / 32, nc = (KB + 7) / 8;
+
+    int* table = reinterpret_cast<int*>(smem + kSTable);
+    const int all = tile_table<kSM>(p, table) * NT, per = (all + 7) >> 3, stride = gridDim.x >> 3;
+    const int end = min(((int)blockIdx.x & 7) * per + per, all);
+    int mine = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+    if (mine >= end) return;
+
+    // ---- loads: a stage at a time, two ahead of the multiplication, over the tiles' ends; lane i of
+    // a 16-byte load fills row i / 8, slot i % 8 (swz8), of a scale load row i / 2, dword i % 2.
+    // Rows and outputs past the tile's end: any valid row.
+    const uint8_t *wbase, *abase, *wsbase, *asbase;
+    int wmax, amax, lmine = mine, lc = 0, lslot = 0;
+    bool more = true;
+    auto load_from = [&](const Tile& n) {
+        const int64_t w0 = (int64_t)n.g * p.N + n.nt * kTN;
+        wbase = p.w + w0 * (p.K / 2);
+        wsbase = p.w_s + w0 * KB;
+        wmax = p.N - 1 - n.nt * kTN;
+        abase = static_cast<const uint8_t*>(p.a) + (int64_t)n.rb * p.K;
+        asbase = p.a_s + (int64_t)n.rb * KB;
+        amax = n.re - 1 - n.rb;
+    };
+    auto load_stage = [&]() {
+        uint8_t* d = smem + lslot * kSStage;
+        const bool whole = lc * 8 + 8 <= KB;
+        auto load = [&](auto bytes, const uint8_t* base, uint32_t off, bool in, uint8_t* dst) {
+            constexpr int B = decltype(bytes)::value;
+            if (whole) load_lds<B>(base, off, dst);
+            else load_lds<B>(within(in, base + off), dst);
+        };
+        constexpr std::integral_constant<int, 16> b16{};
+        constexpr std::integral_constant<int, 4> b4{};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int u = (lane & 7) ^ (lane >> 3) ^ (q & 1), r = wave * 32 + q * 8 + (lane >> 3);
+            load(b16, wbase + (int64_t)lc * 128, min(r, wmax) * (uint32_t)(p.K / 2) + u * 16, lc * 8 + u < KB,
+                 d + (wave * 4 + q) * 1024);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int half = wave >> 2, at = (wave & 3) * 2 + q;
+            const int u = (lane & 7) ^ (lane >> 3) ^ (q & 1), r = at * 8 + (lane >> 3);
+            load(b16, abase + (int64_t)lc * 256, min(r, amax) * (uint32_t)p.K + half * 128 + u * 16,
+                 lc * 256 + half * 128 + u * 16 < p.K, d + kSRows + (half * 8 + at) * 1024);
+        }
+        const int dw = (lane & 1) * 4, half = wave & 1;      // (of the rows' scales four waves load the same)
+        load(b4, wsbase + lc * 8, min(wave * 32 + (lane >> 1), wmax) * (uint32_t)KB + dw, lc * 8 + dw < KB,
+             d + kSWs + wave * 256);
+        load(b4, asbase + lc * 8, min(half * 32 + (lane >> 1), amax) * (uint32_t)KB + dw, lc * 8 + dw < KB,
+             d + kSAs + half * 256);
+        lslot = lslot == 2 ? 0 : lslot + 1;
+        if (++lc < nc) return;
+        lc = 0;
+        lmine += stride;
+        more = lmine < end;
+        if (more) load_from(table_tile<kSM>(p, table, lmine, NT));
+    };
+
+    Tile t = table_tile<kSM>(p, table, mine, NT);
+    load_from(t);
+    load_stage();
+    bool ahead = more;                                   // the stage after the next to multiply is under way
+    if (more) load_stage();
+    int slot = 0;
+    for (;;) {
+        f32x16_t acc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][v] = 0.f;
+        const bool cols = t.nt * kTN + wave * 32 < p.N;
+        const int nv = cols ? (t.re - t.rb + 31) >> 5 : 0;   // 32-row blocks with rows
+        for (int c = 0; c < nc; ++c) {
+            // loads return in order: this stage's are here when at most the next one's are not
+            if (ahead) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kSLoads) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            ahead = more;
+            if (more) load_stage();                      // (into the slot that all have read before the barrier)
+            const uint8_t* S = smem + slot * kSStage;
+            slot = slot == 2 ? 0 : slot + 1;
+            if (!nv) continue;
+            const uint32_t pick = h ? 0x07050301u : 0x06040200u;      // blocks h, 2 + h, 4 + h, 6 + h
+            auto scales = [&](const uint8_t* at) {
+                const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at);
+                return __builtin_amdgcn_perm(v.y, v.x, pick);
+            };
+            const uint32_t ws = scales(S + kSWs + (wave * 32 + r32) * 8);
+            uint32_t as[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) as[i] = scales(S + kSAs + (i * 32 + r32) * 8);
+            auto group = [&](auto m_c) {
+                constexpr int m = decltype(m_c)::value;
+                const u32x4_t w = *reinterpret_cast<const u32x4_t*>(S + swz8(wave * 32 + r32, 2 * m + h));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i >= nv) break;
+                    u32x4_t a[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        a[q] = *reinterpret_cast<const u32x4_t*>(S + kSRows + (m >> 1) * kSM * 128 +
+                                                                 swz8(i * 32 + r32, 4 * (m & 1) + 2 * q + h));
+                    acc[i] = mfma_w4a8_32<m>(w, ws, a[0], a[1], as[i], acc[i]);
+                }
+            };
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            group(std::integral_constant<int, 2>{});
+            group(std::integral_constant<int, 3>{});
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= nv) break;
+            const int row = t.rb + i * 32 + r32, left = p.N - t.nt * kTN - wave * 32;
+            const int64_t el = row * p.os + t.nt * kTN + wave * 32;
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                // the lane's values 4 g .. + 4 are outputs 8 g + 4 h .. + 4
+                if (p.out_dtype == kF32) {
+#pragma unroll
+                    for (int x = g; x < g + 2; ++x)
+                        if (row < t.re)
+                            store4(p.out, kF32, el + 8 * x + 4 * h,
+                                   f32x4_t{acc[i][4 * x], acc[i][4 * x + 1], acc[i][4 * x + 2], acc[i][4 * x + 3]},
+                                   left - 8 * x - 4 * h);
+                    continue;
+                }
+                // the halves of the wave trade: eight outputs a lane, 8 (g + h) .. + 8
+                const u32x2_t lo = pack4(p.out_dtype, acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]);
+                const u32x2_t hi = pack4(p.out_dtype, acc[i][4 * g + 4], acc[i][4 * g + 5], acc[i][4 * g + 6], acc[i][4 * g + 7]);
+                const u32x2_t give = h ? lo : hi;
+                const u32x2_t got = {(uint32_t)__shfl_xor((int)give.x, 32, 64), (uint32_t)__shfl_xor((int)give.y, 32, 64)};
+                const u32x4_t v = h ? u32x4_t{got.x, got.y, hi.x, hi.y} : u32x4_t{lo.x, lo.y, got.x, got.y};
+                if (row >= t.re) continue;
+                const int col = 8 * (g + h);
+                uint16_t* o = static_cast<uint16_t*>(p.out) + el + col;
+                if (col + 8 <= left) {
+                    *reinterpret_cast<u32x4_any_t*>(o) = v;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (col + x < left) o[x] = (uint16_t)(v[x / 2] >> (16 * (x & 1)));
+                }
+            }
+        }
+        mine += stride;
+        if (mine >= end) break;
+        t = table_tile<kSM>(p, table, mine, NT);
+    }
+}
+
+bool product8_dwords(const ProductArgs& p) {
+    return p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
+}
+
+// Short tiles where the weight's bytes are the cost (up to 64 rows a group on average), and as long
+// as they come to about two rounds of the card: one takes half a tall one's time.  Short / tall us:
+// 320 experts of 2048 x 4096 345 / 444 at 48 rows a group, 420 / 455 at 64, 471 / 459 at 72; of 4096 x
+// 1024 193 / 296 and 241 / 304; 16 experts 26 / 42 at 96, 48 / 51 at 192, 68 / 54 at 256; 24 of 1024 x
+// 2048 28 / 31 at 256, 40 / 32 at 384; one product of 768 x 4096 x 4096 26 / 51, of 1280 47 / 52.
+static bool short_tiles(const ProductArgs& p, int cus) {
+    const int64_t NT = (p.N + kTN - 1) / kTN;
+    return p.M <= (int64_t)p.G * 64 || (p.M / kSM + p.G / 2) * NT <= 2 * cus;
+}
+
 hipError_t launch_product8_tiles(const ProductArgs& p, int cus, hipStream_t s) {
-    const bool aligned =
-        p.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(p.w_s) | reinterpret_cast<uintptr_t>(p.a_s)) & 3) == 0;
-    const int64_t grid = min(tile_grid(p, (p.N + kTN - 1) / kTN), (int64_t)max(cus / 8 * 8, 8));   // one workgroup a CU
-    return aligned ? launch_tiles<w4a8_tile_kernel<true>, k8Lds>(p, grid, s)
-                   : launch_tiles<w4a8_tile_kernel<false>, k8Lds>(p, grid, s);
+    const bool dwords = product8_dwords(p);
+    const int NT = (p.N + kTN - 1) / kTN;
+    const int64_t most = max(cus / 8 * 8, 8);            // one workgroup a CU
+    if (dwords && short_tiles(p, cus)) return launch_tiles<w4a8_short_kernel, kSLds>(p, min(tile_grid<kSM>(p, NT), most), s);
+    const int64_t grid = min(tile_grid(p, NT), most);
+    return dwords ? launch_tiles<w4a8_tile_kernel<true>, k8Lds>(p, grid, s)
+                  : launch_tiles<w4a8_tile_kernel<false>, k8Lds>(p, grid, s);
 }
 
 }  // namespace moe
+
+int moe_internal_product8_short(int M, int N, int K, int G, int cus) {
+    moe::ProductArgs p{};
+    p.M = M; p.N = N; p.K = K; p.G = G;
+    return moe::product8_dwords(p) && moe::short_tiles(p, cus);
+}

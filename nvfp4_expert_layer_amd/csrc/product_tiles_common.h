@@ -131,9 +131,10 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& p, int NT, int* s) 
     return t;
 }
 
+template <int TM = kTM>
 static int64_t tile_grid(const ProductArgs& p, int NT) {
     // groups' partial tiles: at most one each
-    const int64_t tiles = p.M / kTM + min(p.G, p.M);
+    const int64_t tiles = p.M / TM + min(p.G, p.M);
     return (tiles * NT + 7) / 8 * 8;
 }
 
@@ -180,8 +181,9 @@ constexpr int scale_bytes(bool aligned, int blocks) { return 256 * blocks * (ali
 constexpr int kWaveStage = 2048;                            // a wave's 32 x 32 outputs on their way out
 constexpr int kTable = (1024 + 1) * 4;
 
-// table[g] = tiles of the groups before g, g = 0 .. G; returns their total.  512
+// table[g] = tiles (of TM rows) of the groups before g, g = 0 .. G; returns their total.  512
 // threads; ends with a barrier.
+template <int TM = kTM>
 __device__ __forceinline__ int tile_table(const ProductArgs& p, int* table) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int n[2];
@@ -189,7 +191,7 @@ __device__ __forceinline__ int tile_table(const ProductArgs& p, int* table) {
     for (int i = 0; i < 2; ++i) {
         int rb = 0, re = 0;
         if (2 * tid + i < p.G) group_rows(p, 2 * tid + i, rb, re);
-        n[i] = (re - rb + kTM - 1) / kTM;
+        n[i] = (re - rb + TM - 1) / TM;
     }
     const int sum = n[0] + n[1];
     int inc = sum;
@@ -212,10 +214,11 @@ __device__ __forceinline__ int tile_table(const ProductArgs& p, int* table) {
     if (tid == 0 && p.G == 1024) table[1024] = total;
     __syncthreads();
     // (offsets that decrease could claim more tiles than the rows hold)
-    return __builtin_amdgcn_readfirstlane(min(total, p.M / kTM + p.G));
+    return __builtin_amdgcn_readfirstlane(min(total, p.M / TM + p.G));
 }
 
 // Tile `logical` (tile-major, NT column blocks a tile) by search in the table.
+template <int TM = kTM>
 __device__ __forceinline__ Tile table_tile(const ProductArgs& p, const int* table, int logical, int NT) {
     const int tile = logical / NT;
     int lo = 0, hi = p.G;
@@ -226,8 +229,8 @@ __device__ __forceinline__ Tile table_tile(const ProductArgs& p, const int* tabl
     }
     int rb, re;
     group_rows(p, lo, rb, re);
-    rb += (tile - __builtin_amdgcn_readfirstlane(table[lo])) * kTM;
-    return Tile{lo, __builtin_amdgcn_readfirstlane(rb), __builtin_amdgcn_readfirstlane(min(rb + kTM, re)),
+    rb += (tile - __builtin_amdgcn_readfirstlane(table[lo])) * TM;
+    return Tile{lo, __builtin_amdgcn_readfirstlane(rb), __builtin_amdgcn_readfirstlane(min(rb + TM, re)),
                 logical - tile * NT};
 }
 

@@ -173,8 +173,9 @@ def test_no_rows():
                          torch.empty(0, 16, device="cuda"))
 
 
-@pytest.mark.parametrize("K", [32, 64, 96, 160, 192, 224, 256, 288, 480, 544, 800])
-@pytest.mark.parametrize("M,N,G", [(3026, 841, 66), (4100, 515, 100), (1200, 4099, 20), (90000, 257, 3)])
+@pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 192, 224, 256, 288, 384, 480, 512, 544, 640, 800, 1280])
+@pytest.mark.parametrize("M,N,G", [(3026, 841, 66), (4100, 515, 100), (1200, 4099, 20), (90000, 257, 3), (6000, 1500, 31),
+                                   (9000, 1100, 40)])
 def test_workgroups_of_several_tiles(M, N, G, K):
     """More tiles than compute units: scale rows that lie differently to dwords in a workgroup's tiles, of one
     chunk of K and more."""
