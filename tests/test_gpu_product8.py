@@ -183,3 +183,31 @@ def test_workgroups_of_several_tiles(M, N, G, K):
     log(f"product8 several tiles M={M} N={N} G={G} K={K}")
     assert not nv.lib().moe_internal_product_streams(M, N, K, G, K, 2, 0, 256)
     check(M, N, K, spread(M, G, K, M - 5))
+
+
+@pytest.mark.parametrize("M,N,K,G", [(3000, 700, 640, 50), (1000, 2048, 1024, 3), (60000, 520, 384, 2)])
+def test_captured_with_other_offsets(M, N, K, G):
+    """One graph of short (or tall) tiles, replayed with other offsets and rows, beside work on another stream."""
+    require_gpu()
+    log(f"product8 captured M={M} N={N} K={K} G={G}")
+    q, w = rows(M, K, 1), weights(G, N, K, 2)
+    p = nv.make_product_problem(M, N, K, G)
+    off = torch.tensor(spread(M, G, 1), dtype=torch.int32, device="cuda")
+    out, want = (torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    nv.moe_mxfp8_product(p, q, w, off, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.moe_mxfp8_product(p, q, w, off, out)
+    side = torch.cuda.Stream()
+    for i in range(5):
+        off.copy_(torch.tensor(spread(M, G, 10 + i, [M, 0, 1, M - 9, M][i]), dtype=torch.int32))
+        q.codes.copy_(rows(M, K, 20 + i).codes)
+        out.fill_(3.0)
+        want.fill_(3.0)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        nv.moe_mxfp8_product(p, q, w, off, want, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+        check(M, N, K, off.tolist(), q=nv.MXFP8Rows(q.codes, q.scales), w=w)
