@@ -74,8 +74,10 @@ int moe_route_backward(const moe_route_problem *p, const void *logits, int64_t l
 /* ------------------------------------------------------------------------- *
  * Norm.  h = x + residual (rounded to the rows' type; h = x without a residual),
  *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight,
- * in fp32: from magnitudes of about 2^63 on the squares' sum passes its range (rstd 0), below
- * 2^-63 they leave no trace beside eps, and with eps 0 a row of zeros has y NaN.
+ * in fp32: a row whose sum of squares passes its range (from magnitudes of 2^64 / sqrt(d) on,
+ * where all are alike: 2^58 at d = 4096) has rstd 0 and y 0; a mean square below 2^-25 eps leaves
+ * no trace.  With eps 0 squares below 2^-126 lose bits, a row whose squares all vanish (magnitudes
+ * below 2^-75) has rstd Inf, and of a row of zeros y is NaN.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t rows;           /* T: 0..2^27                                             */
