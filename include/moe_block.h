@@ -113,7 +113,9 @@ int moe_norm_backward(const moe_norm_problem *p, const void *h, int64_t h_stride
 
 /* ------------------------------------------------------------------------- *
  * SwiGLU.  Rows u [M][2F] hold gate | up (the order of w13's outputs):
- *   a = gate / (1 + exp(-gate)) * up.
+ *   a = gate / (1 + exp(-gate)) * up,
+ * in fp32: from gates of about -88 downwards exp(-gate) passes its range, and a and du are 0 (their
+ * values are below 2^-121 of |up|, and of |da up| and |da|).
  * offsets as the products' (device int32 [groups + 1]): rows from offsets[groups] on are
  * neither read nor written; NULL: all rows.
  * ------------------------------------------------------------------------- */

@@ -41,3 +41,29 @@ def test_norm_magnitudes(dtype, d):
     # beside eps a mean square below 2^-25 of it leaves no trace
     _, rstd = norm(torch.full((1, d), 2.0 ** -24, dtype=dtype, device="cuda"), 2.0 ** -20)
     assert rstd[0] == 2.0 ** 10
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_of_far_gates(dtype):
+    """From gates of about -88 on a and du are 0, whose values are below 2^-121 of |up|, |da up| and |da|."""
+    require_gpu()
+    log(f"swiglu far gates {dtype}")
+    F = 64
+    gate = torch.linspace(-120.0, -70.0, F).to(dtype)
+    u = torch.cat([gate, torch.linspace(-4, 4, F).to(dtype)]).unsqueeze(0)
+    da = torch.linspace(-2, 2, F).to(dtype).unsqueeze(0)
+    p = nv.make_swiglu_problem(1, F, 1, dtype)
+    a, du = torch.empty(1, F, dtype=dtype, device="cuda"), torch.empty(1, 2 * F, dtype=dtype, device="cuda")
+    nv.moe_swiglu(p, u.cuda(), None, a, None, None)
+    nv.moe_swiglu_backward(p, u.cuda(), None, da.cuda(), du)
+    g, up, d = gate.double(), u[0, F:].double(), da[0].double()
+    s = torch.sigmoid(g)
+    want = torch.stack([g * s * up, d * up * s * (1 + g * (1 - s)), d * g * s])
+    mag = torch.stack([up.abs(), (d * up).abs(), d.abs()])
+    got = torch.cat([a, du[:, :F], du[:, F:]]).double().cpu()
+    far = g < -88.8
+    assert (got[:, far] == 0).all() and (want[:, far].abs() <= 2.0 ** -121 * mag[:, far]).all()
+    near = g > -87
+    half, tiny = torch.finfo(dtype).eps / 2, float(torch.finfo(dtype).smallest_normal) * torch.finfo(dtype).eps
+    lim = ((14 + 2 * g[near].abs()) * U * (1 + g[near].abs()) / g[near].abs() * 1.1 + half) * want[:, near].abs() + tiny
+    assert ((got - want)[:, near].abs() <= lim).all()
