@@ -161,8 +161,9 @@ int moe_swiglu_backward(const moe_swiglu_problem *p, const void *u, int64_t u_st
 int moe_mxfp8_quantize(const void *x, int32_t dtype, int64_t R, int32_t C, int64_t x_stride, uint8_t *codes,
                        uint8_t *scales, void *stream);
 
-/* The values: out [R][C] (bf16, f16 or f32), row stride out_stride.  Exact in bf16 and f32
- * up to overflow; rounded to nearest in f16 (overflow gives Inf). */
+/* The values: out [R][C] (bf16, f16 or f32), row stride out_stride.  Exact in f32, and in bf16
+ * under scale bytes from 3 on, up to overflow; rounded to nearest in f16 (overflow gives Inf) and
+ * under the three lowest scale bytes in bf16, whose smallest value 2^-133 is above theirs. */
 int moe_mxfp8_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t R, int32_t C, int32_t dtype, void *out,
                          int64_t out_stride, void *stream);
 

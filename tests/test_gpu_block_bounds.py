@@ -67,3 +67,30 @@ def test_swiglu_of_far_gates(dtype):
     half, tiny = torch.finfo(dtype).eps / 2, float(torch.finfo(dtype).smallest_normal) * torch.finfo(dtype).eps
     lim = ((14 + 2 * g[near].abs()) * U * (1 + g[near].abs()) / g[near].abs() * 1.1 + half) * want[:, near].abs() + tiny
     assert ((got - want)[:, near].abs() <= lim).all()
+
+
+def test_dequantizer_below_bf16():
+    """Exact in f32 for every scale byte; in bf16 from byte 3 on, below it to nearest, ties to even."""
+    require_gpu()
+    log("mxfp8 smallest values")
+    codes = torch.arange(256, dtype=torch.uint8).repeat(8, 1).cuda()
+    scales = torch.arange(8, dtype=torch.uint8).unsqueeze(1).repeat(1, 8).cuda()
+    f, b = torch.empty(8, 256, device="cuda"), torch.empty(8, 256, dtype=torch.bfloat16, device="cuda")
+    nv.moe_mxfp8_dequantize(codes, scales, f)
+    nv.moe_mxfp8_dequantize(codes, scales, b)
+    fine = ~torch.isnan(f)
+    assert fine.sum() == 8 * 254
+    # f32 by the format's own fields
+    c = torch.arange(256).double()
+    e, m = (c.int() >> 3 & 15).double(), (c.int() & 7).double()
+    v = torch.where(e == 0, m / 8 * 2.0 ** -6, (1 + m / 8) * torch.exp2(e - 7)) * torch.where(c >= 128, -1.0, 1.0)
+    want = v * torch.exp2(torch.arange(8).double() - 127).unsqueeze(1)
+    assert torch.equal(f.double().cpu()[fine.cpu()], want[fine.cpu()])
+    same = b.double() == f.double()
+    assert same[3:][fine[3:]].all() and not same[:3][fine[:3]].all()
+    step = 2.0 ** -133                                              # bf16's smallest value: its step down here
+    low = fine & (f.abs() < 2.0 ** -126)
+    err = (b.double() - f.double()).abs() / step
+    assert (err[low] <= 0.5).all()
+    tie = low & (err == 0.5)
+    assert tie.any() and ((b.double()[tie] / step) % 2 == 0).all()
