@@ -94,3 +94,34 @@ def test_dequantizer_below_bf16():
     assert (err[low] <= 0.5).all()
     tie = low & (err == 0.5)
     assert tie.any() and ((b.double()[tie] / step) % 2 == 0).all()
+
+
+@pytest.mark.parametrize("T,d,dtype", [(40, 96, torch.bfloat16), (3, 4096, torch.float32), (700, 32, torch.float16)])
+def test_norm_writes_what_is_asked_for(T, d, dtype):
+    """Every choice of outputs, each between neighbours of one buffer: no byte beside them changes."""
+    require_gpu()
+    log(f"norm outputs between neighbours {dtype} {T}x{d}")
+    x, r = torch.randn(T, d, device="cuda").to(dtype), torch.randn(T, d, device="cuda").to(dtype)
+    w, es = torch.ones(d, device="cuda"), x.element_size()
+    p = nv.make_norm_problem(T, d, 1e-6, dtype, torch.float32)
+    sizes = [T * d * es, T * d * es, T * d, T * (d // 32), T * 4]
+    starts, at = [], 64
+    for n in sizes:
+        starts.append(at)
+        at += (n + 63) // 16 * 16 + 16                              # 32 to 48 bytes between
+    first = None
+    for skip in range(16):
+        buf = torch.full((at,), 0x5A, dtype=torch.uint8, device="cuda")
+        part = [buf[s:s + n] for s, n in zip(starts, sizes)]
+        h, y = (part[i].view(dtype).view(T, d) for i in (0, 1))
+        q, rstd = nv.MXFP8Rows(part[2].view(T, d), part[3].view(T, d // 32)), part[4].view(torch.float32)
+        kept = [None if skip >> i & 1 else v for i, v in enumerate((h, y, q, rstd))]
+        nv.moe_norm(p, x, r, w, *kept)
+        wrote = torch.zeros(at, dtype=torch.bool, device="cuda")
+        for i, s in enumerate((0, 1, 2, 2, 3)):
+            if kept[s] is not None:
+                wrote[starts[i]:starts[i] + sizes[i]] = True
+        assert (buf[~wrote] == 0x5A).all()
+        first = buf if first is None else first                     # all four outputs
+        assert torch.equal(buf[wrote], first[wrote])
+    assert (first != 0x5A).any()
