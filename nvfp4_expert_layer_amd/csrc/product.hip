@@ -472,15 +472,23 @@ static bool tiles_reach(const ProductArgs& p) { return p.as <= (1 << 22); }
 // can pick the slower kernel (W4A16, 160 experts of 2048 x 4096: 3500 rows 198 / 236 spread
 // evenly, 572 / 324 after a Zipf law; 40 of 320 experts, an eighth of 2048 rows kept, 47 / 71).
 //
-// MXFP8 rows in short tiles (scales in dwords), streamed / tiled us: where one row block of every
-// group fills the card twice, 173 / 154 at 8 rows a group (320 of 4096 x 1024), 277 / 269 (320 of 2048
-// x 4096), 51 / 51 at 12 (64 of 2048 x 4096), 322 / 282 at 24; at half a card (16 groups) 18 / 20 at
-// 20, 29 / 21 at 24; at a quarter (8 groups) 24 / 25 at 48, 31 / 25 at 56; at a sixteenth (one group
-// of 4096 x 4096) 24 / 24 at 96, 30 / 24 at 128.
-// In the tall ones one tile alone takes longer (one of K = 4096: 40 us) and streaming wins for more
-// rows: 160 groups of 2048 x 4096 160 / 222 at 32 rows a group, 275 / 236 at 48; 64 groups 60 / 90
-// and 102 / 97; a quarter of the card (8 groups) 37 / 43 at 96, 48 / 43 at 128; a twelfth or less
-// (one group of 4096 x 4096) 45 / 48 at 192, 59 / 49 at 256.
+// MXFP8 rows, streamed / tiled us; `one`: the tiles of one row block of every group.
+// Scales in dwords, K up to 4096 (short tiles).  Two cards of tiles or more: 320 groups of 2048 x 4096
+// 274 / 263 at 8 rows a group, 333 / 284 at 24; of 4096 x 1024 174 / 156 at 8; 64 groups of 2048 x 4096
+// 48 / 50 at 8, 53 / 52 at 14, 73 / 57 at 24.  A third of a card to two: 16 groups 17.8 / 20.2 at 19, 28.8 /
+// 24.3 at 20; 32 groups 23 / 23 at 4, 28 / 24 at 20, 47 / 28 at 28; 20 groups of 4096 x 2048 22 / 23 at 8,
+// 26 / 23 at 20; where the streams' workgroups fill the card unevenly tiles win at every count: 24 groups
+// 30 / 21 at 4, 36 / 21 at 20, 48 groups 43 / 40 and 50 / 41, 12 of 4096 x 1024 14 / 8 and 15 / 9.  A quarter
+// (8 groups) 24 / 24 at 48, 31 / 25 at 56; a sixteenth (one group of 4096 x 4096) 24 / 24 at 96, 31 / 24 at 128.
+// Scales that are no whole dwords, K up to 4096 (tall tiles, of which one alone takes longer: 43 us at
+// K = 4064): 160 groups of 2048 x 4064 233 / 267 at 32, 283 / 274 at 40; 64 groups 103 / 111 at 40, 122 / 113
+// at 48; half a card (16 groups) 30 / 45 at 40, 44 / 46 at 64; a quarter (8 groups) 37 / 47 at 110, 45 / 52 at
+// 128; a sixteenth (one group of 4096 x 4064) 36 / 54 at 200, 41 / 53 at 256.
+// The bounds are those of K up to 4096.  Beyond, the resident tokens are 16 at a time (beyond 8192 none)
+// and the bounds are too high, by up to four times: 160 groups of 2048 x 4128 242 / 258 at 8, 267 / 259 at 12,
+// 503 / 280 at 32; 16 groups 22 / 43 at 8, 59 / 47 at 20; 8 groups 46 / 47 at 48, 90 / 50 at 96; one of 4096 x
+// 4128 47 / 51 at 160, 57 / 55 at 192; in dwords 64 groups of 2048 x 8192 112 / 133 at 8, 16 groups 26 / 36 at
+// 8, 47 / 36 at 12; of 2048 x 8320 201 / 125 and 40 / 39 at 8, one of 4096 x 8320 28 / 44 at 64, 45 / 47 at 96.
 static bool streamed(const ProductArgs& p, int cus) {
     if (p.a8) {
         const int64_t one = (int64_t)p.G * ((p.N + 255) / 256);
