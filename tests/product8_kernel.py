@@ -37,7 +37,9 @@ def weight_values(codes, scales):
     """fp64 values of MXFP4 codes [..., K/2] and scales [..., K/32]."""
     pairs = np.arange(256, dtype=np.uint8)
     table = torch.from_numpy(mxfp4.dequantize(pairs.reshape(16, 16), np.full((16, 1), 127, np.uint8)).reshape(256, 2)).cuda()
-    return table[codes.int()].flatten(-2) * _scale_table()[scales.int()].repeat_interleave(32, -1)
+    # (a gather of pairs at once has given zeros here beyond 2^26 of them)
+    both = torch.stack([table[:, i].contiguous()[codes.int()] for i in (0, 1)], -1).flatten(-2)
+    return both * _scale_table()[scales.int()].repeat_interleave(32, -1)
 
 
 def bound(a, w):
